@@ -1,4 +1,5 @@
-"""MI355X (gfx950) MoE top-k routing, dispatch and combine.
+"""MI355X (gfx950) MoE top-k routing, dispatch and combine, and the
+experts' products between them with their gradients.
 
 The hot path runs in hand-written HIP kernels in ``libmoe_route.so`` behind a
 C ABI (``include/moe_route.h``); this package is the thin torch binding.
@@ -23,6 +24,15 @@ from .binding import (  # noqa: F401
     moe_route_dispatch_workspace_bytes,
     moe_route_topk,
     moe_route_topk_grouped,
+)
+from .experts import (  # noqa: F401
+    GatedGrads,
+    MatmulGrads,
+    moe_combine_backward,
+    moe_expert_gated,
+    moe_expert_gated_backward,
+    moe_expert_matmul,
+    moe_expert_matmul_backward,
 )
 
 _lib.load()

@@ -41,7 +41,20 @@ SIGNATURES = {
     "moe_route_dispatch_fp8": (_c_int, [_vp, _vp, _c_i64, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
                                         _c_i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                         _c_i64, _vp, _c_size, _vp]),
+    "moe_expert_gated": (_c_int, [_vp, _vp, _vp, _c_i64, _c_i32, _c_i32, _c_i32, _c_i32, _vp, _vp,
+                                  _vp]),
+    "moe_expert_gated_backward": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_i64, _c_i32, _c_i32,
+                                           _c_i32, _c_i32, _vp, _vp, _vp, _c_i32, _vp]),
+    "moe_expert_matmul": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_i64, _c_i32, _c_i32, _c_i32,
+                                   _c_i32, _vp, _vp, _vp]),
+    "moe_expert_matmul_backward": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_i64, _c_i32, _c_i32,
+                                            _c_i32, _c_i32, _vp, _vp, _vp, _c_i32, _vp, _vp]),
+    "moe_combine_backward": (_c_int, [_vp, _vp, _vp, _vp, _c_i64, _c_i32, _c_i32, _c_i64, _vp,
+                                      _vp, _vp]),
 }
+
+# enum moe_act
+ACTS = {"none": 0, "silu": 1, "gelu": 2, "relu": 3}
 
 MOE_OK = 0
 MOE_ERR_INVALID_ARG = -1

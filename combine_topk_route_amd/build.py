@@ -8,10 +8,12 @@ import os
 import shutil
 import subprocess
 import sys
+from typing import Optional
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 SRC = os.path.join(PKG_DIR, "csrc", "moe_route.hip")
+EXPERTS_SRC = os.path.join(PKG_DIR, "csrc", "moe_experts.hip")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG_DIR, "libmoe_route.so")
 ARCH = "gfx950"
@@ -24,15 +26,16 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found (ROCm is required to build libmoe_route.so)")
 
 
-def command(out: str = LIB, defines: tuple = (), src: str = SRC) -> list[str]:
-    """hipcc command line; ``defines`` (e.g. ``("MOE_RECV_SLICES=1",)``) build
-    the measurement variants that probes.py compares against the library,
-    and ``src`` its own measurement kernels."""
+def command(out: str = LIB, defines: tuple = (), src: Optional[str] = None) -> list[str]:
+    """hipcc command line of the library; ``defines`` (e.g.
+    ``("MOE_RECV_SLICES=1",)``) build the measurement variants that probes.py
+    compares against the library, and ``src`` its own measurement kernels."""
+    sources = [SRC, EXPERTS_SRC] if src is None else [src]
     return [
         hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
         # keep the compiler from forming packed fp32 VALU ops
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-        "-Wall", f"-I{INCLUDE}", *[f"-D{d}" for d in defines], "-o", out, src,
+        "-Wall", f"-I{INCLUDE}", *[f"-D{d}" for d in defines], "-o", out, *sources,
     ]
 
 
@@ -83,8 +86,8 @@ def variant_path(name: str, lib: str = "libmoe_route.so") -> str:
     return os.path.join(VARIANT_DIR, name, lib)
 
 
-def build_variant(name: str, defines: tuple, verbose: bool = False, src: str = SRC,
-                  lib: str = "libmoe_route.so") -> str:
+def build_variant(name: str, defines: tuple, verbose: bool = False,
+                  src: Optional[str] = None, lib: str = "libmoe_route.so") -> str:
     """The library built with measurement ``defines`` (another slice count
     or store form for the recv kernel), or another measurement source, as
     _build/<name>/<lib>, for probes.py only (never loaded by the package)."""

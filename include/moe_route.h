@@ -353,6 +353,131 @@ int moe_combine(const void* y, const int32_t* pair_row, const float* topk_w,
                 int64_t T, int32_t H, int32_t k, int64_t capacity, void* out,
                 void* stream);
 
+/*
+ * The experts: the products between dispatch and combine, and their gradients
+ * ---------------------------------------------------------------------------
+ * Every call takes rows in dispatch's order: expert e's rows are
+ * [expert_offsets[e], expert_offsets[e+1]) of a buffer of `rows` rows, so
+ * that dispatch's `buf` and `expert_offsets` go straight in and what comes out
+ * goes straight into combine ("Lower latency and higher throughput with
+ * multi-node DeepSeek deployment", section "GroupGEMM": one product per expert
+ * over the tokens it received).
+ *
+ *  - rows is a host-side bound (0 <= rows < 2^31): launches depend on it, on E
+ *    and on the feature sizes only, so a captured graph serves any routing.
+ *  - expert_offsets [E+1] int32 is read on the device.  Offsets outside
+ *    [0, rows] are held to it; an expert whose end is not past its start has
+ *    no rows.  Rows outside every expert (behind expert_offsets[E]) are left
+ *    as they were in every output.
+ *  - Features (H, I, K, N) are multiples of 8 between 8 and 2^20; every bf16
+ *    pointer is 16-byte aligned.  1 <= E <= 1024.
+ *  - Rows and weights are bf16; products accumulate in fp32 and each output is
+ *    rounded once, from fp32.  The order of a sum does not depend on the
+ *    timing of the run: repeated calls give the same bits.
+ *  - Outputs must not overlap inputs, except that `residual` may be `y`.
+ */
+enum moe_act {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_SILU = 1, /* z / (1 + exp(-z))                                    */
+  MOE_ACT_GELU = 2, /* z * Phi(z), Phi the normal distribution function     */
+  MOE_ACT_RELU = 3  /* max(z, 0); its slope at 0 is 0                        */
+};
+
+/*
+ * moe_expert_gated - the gated block's two projections, the activation and
+ * their product in one launch:
+ *
+ *   gate = x W_gate[e]^T,  up = x W_up[e]^T,  h = act(gate) * up
+ *
+ *   x          [rows, H] bf16.
+ *   w_gate_up  [E, 2*I, H] bf16: of each expert the I gate rows, then the I up
+ *              rows.
+ *   act        MOE_ACT_SILU, MOE_ACT_GELU or MOE_ACT_RELU.
+ *   h          [rows, I] bf16 (out), from the unrounded factors.
+ *   gate_up    [rows, 2*I] bf16 (out) or NULL: gate, then up, as
+ *              moe_expert_gated_backward takes them.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_ALIGNMENT (a feature size that is no
+ *         multiple of 8, a misaligned pointer).
+ */
+int moe_expert_gated(const void* x, const int32_t* expert_offsets, const void* w_gate_up,
+                     int64_t rows, int32_t E, int32_t H, int32_t I, int32_t act,
+                     void* h, void* gate_up, void* stream);
+
+/*
+ * moe_expert_gated_backward - gradients of moe_expert_gated:
+ *
+ *   dgate = dh * up * act'(gate),  dup = dh * act(gate)
+ *   dx = [dgate dup] W[e],  dW[e] = [dgate dup]^T x over the expert's rows
+ *
+ *   dh, gate_up, x, w_gate_up  as the forward call has them.
+ *   dgate_up   [rows, 2*I] bf16 (out).  dx and dW are formed from it as it is
+ *              stored: the matrix instruction takes 16-bit operands, and the
+ *              rounding adds one error of the size of dx's own.
+ *   dx         [rows, H] bf16 (out) or NULL.
+ *   dw         [E, 2*I, H] (out) or NULL: bf16, or fp32 with dw_f32 = 1.  An
+ *              expert without rows gets zeros, also with rows == 0.
+ * x may be NULL without dw, w_gate_up without dx.
+ */
+int moe_expert_gated_backward(const void* dh, const void* gate_up, const void* x,
+                              const int32_t* expert_offsets, const void* w_gate_up,
+                              int64_t rows, int32_t E, int32_t H, int32_t I, int32_t act,
+                              void* dgate_up, void* dx, void* dw, int32_t dw_f32, void* stream);
+
+/*
+ * moe_expert_matmul - one product per expert with its epilogue:
+ *
+ *   pre = x W[e]^T + bias[e],  y = act(pre) + residual
+ *
+ *   x         [rows, K] bf16;  w [E, N, K] bf16.
+ *   bias      [E, N] bf16 or NULL;  residual [rows, N] bf16 or NULL (it may be y).
+ *   y         [rows, N] bf16 (out), rounded once after the residual.
+ *   pre       [rows, N] bf16 (out) or NULL, as moe_expert_matmul_backward
+ *             takes it.
+ */
+int moe_expert_matmul(const void* x, const int32_t* expert_offsets, const void* w,
+                      const void* bias, const void* residual, int64_t rows, int32_t E, int32_t K,
+                      int32_t N, int32_t act, void* y, void* pre, void* stream);
+
+/*
+ * moe_expert_matmul_backward - gradients of moe_expert_matmul (the residual's
+ * is dy itself):
+ *
+ *   dpre = dy * act'(pre),  dx = dpre W[e],  dW[e] = dpre^T x,
+ *   dbias[e] = sum of dpre over the expert's rows
+ *
+ *   pre, dpre [rows, N] bf16: both needed unless act is MOE_ACT_NONE, where
+ *             dpre is dy and neither is touched.  dx and dW are formed from
+ *             dpre as stored, dbias from its unrounded values.
+ *   dx        [rows, K] bf16 (out) or NULL.
+ *   dw        [E, N, K] (out) or NULL: bf16, or fp32 with dw_f32 = 1.
+ *   dbias     [E, N] fp32 (out) or NULL.
+ * dw and dbias of an expert without rows are zeros, also with rows == 0.
+ */
+int moe_expert_matmul_backward(const void* dy, const void* pre, const void* x,
+                               const int32_t* expert_offsets, const void* w, int64_t rows,
+                               int32_t E, int32_t K, int32_t N, int32_t act, void* dpre,
+                               void* dx, void* dw, int32_t dw_f32, float* dbias, void* stream);
+
+/*
+ * moe_combine_backward - gradients of moe_combine:
+ *
+ *   dy[pair_row[t,j]] = bf16_rne(topk_w[t,j] * dout[t])
+ *   dtopk_w[t,j] = sum over h of dout[t,h] * y[pair_row[t,j], h]   (fp32)
+ *
+ *   dout      [T, H] bf16;  y [capacity, H] bf16;  pair_row, topk_w as in
+ *             moe_combine (the rows of pair_row distinct, as dispatch makes
+ *             them).
+ *   dy        [capacity, H] bf16 (out): rows no pair maps to are untouched.
+ *   dtopk_w   [T, k] fp32 (out): 0 for a pair whose row is outside
+ *             [0, capacity), which combine skips.
+ * dispatch's own gradient needs no call of its own: it is moe_combine of the
+ * rows' gradients with unit weights.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_ALIGNMENT, MOE_ERR_CAPACITY.
+ */
+int moe_combine_backward(const void* dout, const void* y, const int32_t* pair_row,
+                         const float* topk_w, int64_t T, int32_t H, int32_t k, int64_t capacity,
+                         void* dy, float* dtopk_w, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
