@@ -114,16 +114,23 @@ struct Tile {
 
 // Blocks are handed to the 8 XCDs in turn, and each XCD has an L2 of its own.
 // So that the tiles an XCD works on at one time share their operands, tile
-// numbers go to the XCDs in runs of `kRun` (its 32 CUs), or shorter ones where
-// there are too few tiles to give each XCD a run.  A bijection on every 8 * kRun
-// numbers; grids are rounded up to that.
-constexpr int kXcds = 8, kRun = 32;
+// numbers go to the XCDs in runs of 32 (its CUs), and what is left of `total`
+// after the last round of such runs in runs half as long, and so on: a bijection
+// on [0, total).  From `total` on the number is returned as it is.
+constexpr int kXcds = 8;
 
 __device__ __forceinline__ int64_t xcd_order(int64_t id, int64_t total) {
-  int run = kRun;
-  while (run > 1 && total < int64_t(kXcds) * run) run >>= 1;
-  const int64_t j = id / kXcds;
-  return (j / run * kXcds + id % kXcds) * run + j % run;
+  int64_t base = 0;
+#pragma unroll
+  for (int run = 32; run >= 1; run >>= 1) {
+    const int64_t span = (total - base) / (kXcds * run) * (kXcds * run);
+    if (id < base + span) {
+      const int64_t i = id - base, j = i / kXcds;
+      return base + (j / run * kXcds + i % kXcds) * run + j % run;
+    }
+    base += span;
+  }
+  return id;
 }
 
 // Tile `local` of a grid of mt x nt tiles: strips of 8 row tiles, inside a strip
@@ -136,50 +143,71 @@ __device__ __forceinline__ void grid_order(int64_t local, int64_t mt, int64_t nt
   n = rem / gm;
 }
 
-// The tile of block number `id`.  Every thread of the block calls it.
+// Inclusive prefix sum over the 64 lanes: four shifts inside each 16-lane row, then each row's total
+// into the rows above it.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_or_zero(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_prefix(int v) {
+  v += dpp_or_zero<0x111, 0xF>(v);  // row_shr:1
+  v += dpp_or_zero<0x112, 0xF>(v);
+  v += dpp_or_zero<0x114, 0xF>(v);
+  v += dpp_or_zero<0x118, 0xF>(v);
+  v += dpp_or_zero<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
+  v += dpp_or_zero<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
+  return v;
+}
+
+// The tile of block number `id`.  Every thread of the block calls it.  Each thread counts the row
+// tiles of `kPer` experts; the one that holds the tile writes it down.  At most 2^31 / 64 + 1024 row
+// tiles, so the counts fit 32 bits.
 template <int BM, int THREADS>
 __device__ Tile find_tile(const int32_t* off, int E, int64_t rows, int ncol, int64_t id) {
-  __shared__ int64_t s_wave[THREADS / kWave];
+  constexpr int kPer = kMaxE / THREADS, kWaves = THREADS / kWave;
+  __shared__ int s_wave[kWaves];
   __shared__ Tile s_tile;
-  const int per = (E + THREADS - 1) / THREADS;
-  const int e0 = threadIdx.x * per;
-  int64_t mine = 0;
-  for (int i = 0; i < per && e0 + i < E; ++i) {
-    int64_t lo, n;
-    expert_rows(off, e0 + i, rows, lo, n);
-    mine += (n + BM - 1) / BM;
+  int64_t lo[kPer];
+  int n[kPer], mine = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = threadIdx.x * kPer + i;
+    int64_t cnt = 0;
+    lo[i] = 0;
+    if (e < E) expert_rows(off, e, rows, lo[i], cnt);
+    n[i] = int(cnt);
+    mine += int((cnt + BM - 1) / BM);
   }
-  int64_t incl = mine;
-  for (int d = 1; d < kWave; d <<= 1) {
-    const int64_t up = __shfl_up(incl, d);
-    if (lane_id() >= d) incl += up;
-  }
+  const int incl = wave_prefix(mine);
   const int w = threadIdx.x / kWave;
   if (threadIdx.x == 0) s_tile.e = -1;
   if (lane_id() == kWave - 1) s_wave[w] = incl;
   __syncthreads();
-  int64_t pre = incl - mine, total = 0;
+  int pre = incl - mine, total = 0;
 #pragma unroll
-  for (int i = 0; i < THREADS / kWave; ++i) {
-    if (i < w) pre += s_wave[i];
-    total += s_wave[i];
+  for (int i = 0; i < kWaves; ++i) {
+    const int v = s_wave[i];
+    if (i < w) pre += v;
+    total += v;
   }
-  const int64_t seq = xcd_order(id, total * ncol);
-  if (seq >= pre * ncol && seq < (pre + mine) * ncol) {
-    for (int i = 0; i < per && e0 + i < E; ++i) {
-      int64_t lo, n;
-      expert_rows(off, e0 + i, rows, lo, n);
-      const int64_t mt = (n + BM - 1) / BM;
-      if (seq < (pre + mt) * ncol) {
-        int64_t m, c;
-        grid_order(seq - pre * ncol, mt, ncol, m, c);
-        s_tile.e = e0 + i;
-        s_tile.row0 = lo + m * BM;
-        s_tile.rows = int(n - m * BM < BM ? n - m * BM : BM);
-        s_tile.nt = int(c);
-        break;
+  const int64_t tiles = int64_t(__builtin_amdgcn_readfirstlane(total)) * ncol;
+  if (id < tiles) {
+    const int64_t seq = xcd_order(id, tiles);
+    int64_t local = seq - int64_t(pre) * ncol;
+    if (local >= 0 && local < int64_t(mine) * ncol) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int mt = int((int64_t(n[i]) + BM - 1) / BM);
+        if (local >= 0 && local < int64_t(mt) * ncol) {
+          int64_t m, c;
+          grid_order(local, mt, ncol, m, c);
+          s_tile.e = threadIdx.x * kPer + i;
+          s_tile.row0 = lo[i] + m * BM;
+          s_tile.rows = int(n[i] - m * BM < BM ? n[i] - m * BM : BM);
+          s_tile.nt = int(c);
+        }
+        local -= int64_t(mt) * ncol;
       }
-      pre += mt;
     }
   }
   __syncthreads();
@@ -205,17 +233,13 @@ __device__ Tile find_tile(const int32_t* off, int E, int64_t rows, int ncol, int
 // (a 0 against another expert's NaN would not do).
 //
 //   k contiguous (KC): LDS row = position, 128 bytes = 64 k = 8 chunks; chunk c
-//     of row r sits in slot c ^ swizzle(r), so that the 8 lanes that a 128-bit
-//     read serves at once, rows apart by 128 bytes, find 8 different slots.
+//     of row r sits in slot c ^ (r & 7), so that lanes that a 128-bit read serves
+//     at once, rows apart by 128 bytes, find different banks.
 //   position contiguous: LDS row = k, R positions; read transposed
 //     (ds_read_b64_tr_b16: 16 lanes read 4 rows of 16 values and each receives
-//     one column).  Again the chunk order of a row depends on k, so that the 4
-//     rows' pieces lie in different banks.
-//
-// Which position belongs to which row of the matrix instruction is free.  On the
-// P side (PERM) row i of fragment f of a pair stands for position
-// 8 (i / 4) + 4 f + i % 4 of 32, so that a lane's two fragments hold 8 consecutive
-// positions and leave in one 16-byte store.
+//     one column).  32 lanes are served at once, 8 rows; chunk c of row k sits
+//     in slot c ^ (2 (k & 3) + (k & 8)), which puts their 8 pieces of 32 bytes
+//     in different banks of the 64.
 
 constexpr int kBK = 64;
 constexpr uint32_t kOutside = 0x80000000u;  // past every resource (at most 2^30 bytes)
@@ -243,8 +267,7 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t voff, i32x4 r
       "s_nop 0\n\t"
       "buffer_load_dwordx4 %1, %2, %3 offen lds"
       :
-      : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-      : "m0");
+      : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff));
 }
 
 // All but the newest N loads of this wave have arrived and its LDS reads are
@@ -260,163 +283,258 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 }
 
 // One side of R positions, loaded by W waves.
-template <bool KC_, bool PERM, int R, int W>
+template <bool KC_, int R, int W, bool TWO = false>
 struct Side {
   static constexpr bool KC = KC_;
   static constexpr int kBytes = R * kBK * 2;
   static constexpr int kLoads = kBytes / 1024 / W;  // a wave's loads per stage
   static constexpr int kKRows = 512 / R;            // !KC: values of k in one load
+  static constexpr int kRow = R * 2;                // !KC: bytes of an LDS row
 
   uint32_t voff[kLoads];
+  i32x4 rsrc, rsrc2;  // KC: of the positions whose bit 5 is clear / set (they differ if gated)
   const uint16_t* base;
-  const uint16_t* base2;  // KC: base of the positions whose bit 5 is set (gated), or base
   int64_t ld;
-  int64_t K;
-  uint32_t bytes;  // KC: bytes of the valid rows;  else: bytes in front of the first column
-  int kc;          // KC: this lane's k in the stage
+  int whole, tail;  // stages full of k, and the k left for one more
+  uint32_t stage_bytes;
+  uint32_t skip;  // !KC: bytes in front of the first column
+  int kc;         // KC: this lane's k in the stage
 
-  // `base` points at position 0, k 0.  KC: `valid` rows from there exist.  GATED: positions
-  // 32 s + j, s odd, are row 16 (s - 1) + j behind `second`, s even those behind `base`.
-  template <bool GATED>
-  __device__ __forceinline__ void init(const uint16_t* first, const uint16_t* second, int64_t ld_,
-                                       int64_t K_, int64_t valid) {
-    base = first;
-    base2 = second;
+  // KC: `first` points at position 0, k 0, and `valid` rows from there exist.  TWO: positions
+  // 64 s + j are row 32 s + j behind `first` (j < 32) or row 32 s + j - 32 behind `second`.
+  __device__ __forceinline__ void init_kc(const uint16_t* first, const uint16_t* second,
+                                          int64_t ld_, int64_t K_, int64_t valid) {
     ld = ld_;
-    K = K_;
+    whole = __builtin_amdgcn_readfirstlane(int(K_ / kBK));
+    tail = __builtin_amdgcn_readfirstlane(int(K_ % kBK));
+    const uint32_t bytes = valid <= 0 ? 0u : uint32_t(valid < R ? valid : R) * uint32_t(ld * 2);
+    rsrc = resource(first, bytes);
+    rsrc2 = TWO ? resource(second, bytes) : rsrc;
+    const int w = wave_id(), l = lane_id();
+    const int c = (l % 8) ^ (l / 8);
+    kc = c * 8;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int r = (j * W + w) * 8 + l / 8;
+      const int pos = TWO ? (r / 64) * 32 + r % 32 : r;
+      voff[j] = uint32_t(pos) * uint32_t(ld * 2) + c * 16;
+    }
+  }
+
+  // !KC: `first` points at k 0 of the first position, which is column `col` of its row.
+  __device__ __forceinline__ void init_mc(const uint16_t* first, int64_t ld_, int64_t K_, int col) {
+    base = first;
+    ld = ld_;
+    whole = __builtin_amdgcn_readfirstlane(int(K_ / kBK));
+    tail = __builtin_amdgcn_readfirstlane(int(K_ % kBK));
+    skip = __builtin_amdgcn_readfirstlane(col * 2);
+    stage_bytes = kBK * uint32_t(ld * 2) - skip;
     const int w = wave_id(), l = lane_id();
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
-      const int t = j * W + w;
-      if (KC) {
-        const int r = t * 8 + l / 8;
-        const int swz = PERM ? (r & 3) | ((r >> 1) & 4) : r & 7;
-        const int c = (l % 8) ^ swz;
-        kc = c * 8;  // the same for every j: W is even
-        const int pos = GATED ? (r / 64) * 32 + r % 32 : r;
-        voff[j] = uint32_t(pos) * uint32_t(ld * 2) + c * 16;
-      } else {
-        const int k = t * kKRows + l / (R / 8);
-        const int g = PERM ? (k & 3) << 2 : (k & 3) << 1;
-        voff[j] = uint32_t(k) * uint32_t(ld * 2) + ((l % (R / 8)) ^ g) * 16;
-      }
+      const int k = (j * W + w) * kKRows + l / (R / 8);
+      const int g = ((k & 3) << 1) | (k & 8);
+      voff[j] = uint32_t(k) * uint32_t(ld * 2) + ((l % (R / 8)) ^ g) * 16;
     }
-    if (KC)
-      bytes = valid <= 0 ? 0u : uint32_t(valid < R ? valid : R) * uint32_t(ld * 2);
-    else
-      bytes = uint32_t(valid * 2);  // here `valid` is the first column's index in its row
   }
 
-  // Start filling the stage at LDS address `lds` with k in [it * 64, it * 64 + 64).
-  __device__ __forceinline__ void issue(uint32_t lds, int64_t it) const {
-    const int w = wave_id();
-    const int64_t k0 = it * kBK;
-    if (KC) {
-      const i32x4 r0 = resource(base, bytes);
-      const i32x4 r1 = resource(base2, bytes);
-      const bool whole = k0 + kBK <= K;
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        const int t = j * W + w;
-        const uint32_t v = whole || k0 + kc < K ? voff[j] : kOutside;
-        load_to_lds(lds + t * 1024, v, (t >> 2) & 1 ? r1 : r0, whole ? int(k0 * 2) : (k0 < K ? int(k0 * 2) : 0));
-      }
+  // The resource that a stage's loads go through: the k of stage `it` (!KC), or the side's own.
+  template <bool WHOLE>
+  __device__ __forceinline__ i32x4 stage_resource(int it) const {
+    if constexpr (KC) return rsrc;
+    const uint32_t n = WHOLE || it < whole ? stage_bytes
+                       : it == whole && tail > 0 ? uint32_t(tail) * uint32_t(ld * 2) - skip : 0u;
+    return resource(base + (WHOLE || it <= whole ? int64_t(it) * kBK * ld : 0), n);
+  }
+
+  // Start this wave's load J of the stage at `lds` (this wave's first KiB of the side there), which
+  // takes k in [64 it, 64 it + 64).  WHOLE: all of these exist.
+  template <int J, bool WHOLE>
+  __device__ __forceinline__ void issue(uint32_t lds, i32x4 r, int it) const {
+    if constexpr (!KC) {
+      load_to_lds(lds + J * W * 1024, voff[J], r, 0);
     } else {
-      const int64_t rem = K - k0 < kBK ? K - k0 : kBK;
-      const uint32_t n = rem <= 0 ? 0u : uint32_t(rem) * uint32_t(ld * 2) - bytes;
-      const i32x4 r = resource(base + (rem <= 0 ? 0 : k0 * ld), n);
+      if (TWO && (W < 8 ? J & 1 : wave_id() >> 2)) r = rsrc2;
+      const bool some = WHOLE || it <= whole;
+      const uint32_t v = WHOLE || it < whole || (it == whole && kc < tail) ? voff[J] : kOutside;
+      load_to_lds(lds + J * W * 1024, v, r, some ? it * (kBK * 2) : 0);
+    }
+  }
+
+  // Where this lane reads in the side's part of a stage, by half stage (KC) or fragment: the address
+  // of fragment 0, or of the first 128 / STEP fragments (256 bytes on, the swizzle is the same).  Fragment f is positions row0 + f * STEP .. + 15.
+  static constexpr int kBases = KC ? 2 : 8;
+  template <int STEP>
+  static __device__ __forceinline__ void read_bases(uint32_t (&at)[kBases], uint32_t lds, int row0) {
+    const int l = lane_id(), i = l % 16, q = l / 16;
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) load_to_lds(lds + (j * W + w) * 1024, voff[j], r, 0);
+    for (int u = 0; u < (KC ? 2 : 128 / STEP); ++u) {
+      if (KC) {
+        at[u] = lds + (row0 + i) * 128 + (((u * 4 + q) ^ (i & 7)) * 16);
+      } else {
+        const int chunk = (row0 + u * STEP) / 8 + (i % 4) / 2;
+        at[u] = lds + (q * 8 + i / 4) * kRow +
+                ((chunk ^ (((i / 4) << 1) | ((q & 1) << 3))) * 16) + (i & 1) * 8;
+      }
+    }
+  }
+
+  // Fragment F of half stage SUB, 8 values of k per lane, of the stage `at` was moved to.
+  template <int F, int STEP, int SUB>
+  static __device__ __forceinline__ bf16x8 read(const uint32_t (&at)[kBases]) {
+    typedef __attribute__((address_space(3))) const bf16x8* Frag;
+    typedef __attribute__((address_space(3))) s16x4* Tr;
+    if constexpr (KC) {
+      return *reinterpret_cast<Frag>(at[SUB] + F * STEP * 128);
+    } else {
+      constexpr int kPer = 128 / STEP;
+      const uint32_t p = at[F % kPer] + (F / kPer * 256 + SUB * 32 * kRow);
+      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<Tr>(p));
+      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<Tr>(p + 4 * kRow));
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   }
 };
 
-typedef __attribute__((address_space(3))) const bf16x8* LdsFrag;
-typedef __attribute__((address_space(3))) s16x4* LdsTr;
-
-__device__ __forceinline__ bf16x8 read_frag(uint32_t at) {
-  return *reinterpret_cast<LdsFrag>(at);
-}
-// 4 values of k from `at`, the next 4 from `at` + 4 rows.
-template <int ROW>
-__device__ __forceinline__ bf16x8 read_frag_tr(uint32_t at) {
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<LdsTr>(at));
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<LdsTr>(at + 4 * ROW));
-  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+// f(integral_constant<int, 0>) .. f(integral_constant<int, N - 1>)
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void static_for(F f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for<N, I + 1>(f);
+  }
 }
 
 // The tile shape: BM x BN outputs by WM x WN waves, each (BM / WM) x 64, ST stages in LDS.
 // A wave's row fragment i covers rows 16 (i * WM + wave row), so that a short tile loads every
 // wave alike.
-template <int BM_, int BN_, int WM_, int ST_>
+template <int BM_, int BN_, int WM_, int WN_, int ST_>
 struct Shape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = BN_ / 64, ST = ST_;
-  static constexpr int W = WM * WN, kThreads = W * kWave, MR = BM / WM / 16;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_;
+  static constexpr int W = WM * WN, kThreads = W * kWave;
+  static constexpr int kWaveN = BN / WN, MR = BM / WM / 16, NR = kWaveN / 16;
 };
 
-// acc[i][2 p + f] of MREP row fragments: position n = 64 wn + 32 p + 8 (lane / 16) + 4 f + 0..3
-// against row m = 16 (i * WM + wm) + lane % 16.
+// A value that the compiler takes as it finds it: what is added to it stays in the offsets of the
+// instructions that use it.
+__device__ __forceinline__ uint32_t opaque(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+__device__ __forceinline__ int opaque_scalar(int v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
+
+// acc[a][u]: positions 16 u + 4 (lane / 16) .. + 3 of the wave's, against row lane % 16 of its row
+// fragment a, for MREP row fragments.
+//
+// A step takes one stage in two halves of MREP groups of 4 matrix instructions.  While a half is
+// computed the next half's fragments are read, each row fragment into the registers that the group
+// before has just used.  The second half reads from the next stage: kHead groups into it stands the
+// barrier that hands that stage over, so that these groups cover the end of the reads and the
+// barrier.  With it the current stage has been read by all, and the loads of the stage ST further on
+// go into its place, spread over the rest of the half: issued together they hold up every wave for
+// as long as the CU's one address unit takes for all of them.
 template <typename S, int MREP, typename PS, typename QS>
-__device__ __forceinline__ void product(f32x4 (&acc)[MREP][4], uint8_t* smem, const PS& P,
+__device__ __forceinline__ void product(f32x4 (&acc)[MREP][S::NR], uint8_t* smem, const PS& P,
                                         const QS& Q, int64_t K) {
-  static_assert(S::WM == 2, "the position-contiguous row offsets assume two wave rows");
   constexpr int kStage = PS::kBytes + QS::kBytes;
   constexpr int kLoads = PS::kLoads + QS::kLoads;
-  constexpr int kPRow = S::BN * 2, kQRow = S::BM * 2;
+  constexpr int kHead = MREP >= 4 ? 2 : 1, kStep = 16 * S::WM;
   const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_address(smem));
   const int w = wave_id(), wm = w % S::WM, wn = w / S::WM;
-  const int l = lane_id(), i = l % 16, q = l / 16;
 #pragma unroll
   for (int a = 0; a < MREP; ++a)
 #pragma unroll
-    for (int b = 0; b < 4; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // where this lane reads, in a stage
-  uint32_t pb[2], qb[2];
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    pb[u] = PS::KC ? wn * 8192 + ((i / 4) * 8 + i % 4) * 128 +
-                         (((u * 4 + q) ^ ((i & 3) | (i & 4))) * 16)
-                   : (q * 8 + i / 4) * kPRow + (((wn * 8 + u * 4 + i % 4) ^ ((i / 4) << 2)) * 16);
-    qb[u] = PS::kBytes +
-            (QS::KC ? (wm * 16 + i) * 128 + (((u * 4 + q) ^ (i & 7)) * 16)
-                    : (q * 8 + i / 4) * kQRow +
-                          (((u * 4 + wm * 2 + (i % 4) / 2) ^ ((i / 4) << 1)) * 16) + (i & 1) * 8);
-  }
-  const int64_t n = (K + kBK - 1) / kBK;
+    for (int b = 0; b < S::NR; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int n = int((K + kBK - 1) / kBK);
   if (n == 0) return;
+  uint32_t pb[PS::kBases], qb[QS::kBases], pat[PS::kBases], qat[QS::kBases];
+  PS::template read_bases<16>(pb, lds, wn * S::kWaveN);
+  QS::template read_bases<kStep>(qb, lds + PS::kBytes, wm * 16);
+  auto move_to = [&](int stage) {
 #pragma unroll
-  for (int s = 0; s < S::ST - 1; ++s) {
-    P.issue(lds + s * kStage, s);
-    Q.issue(lds + s * kStage + PS::kBytes, s);
+    for (int u = 0; u < (PS::KC ? 2 : 8); ++u) pat[u] = opaque(pb[u] + stage * kStage);
+#pragma unroll
+    for (int u = 0; u < (QS::KC ? 2 : 128 / kStep); ++u) qat[u] = opaque(qb[u] + stage * kStage);
+  };
+  const int dest = opaque_scalar(lds + w * 1024);
+  auto load = [&](auto j, auto whole, int stage, int it, i32x4 pr, i32x4 qr) {
+    if constexpr (j < PS::kLoads)
+      P.template issue<j, whole>(dest + stage * kStage, pr, it);
+    else
+      Q.template issue<j - PS::kLoads, whole>(dest + stage * kStage + PS::kBytes, qr, it);
+  };
+  constexpr std::integral_constant<bool, false> kChecked{};
+#pragma unroll
+  for (int st = 0; st < S::ST; ++st) {
+    const i32x4 pr = P.template stage_resource<false>(st), qr = Q.template stage_resource<false>(st);
+    static_for<kLoads>([&](auto j) { load(j, kChecked, st, st, pr, qr); });
   }
-  int cur = 0;
-  for (int64_t it = 0; it < n; ++it) {
-    stage_ready<(S::ST - 2) * kLoads>();
-    const int to = cur == 0 ? S::ST - 1 : cur - 1;  // the stage read in the last step
-    P.issue(lds + to * kStage, it + S::ST - 1);
-    Q.issue(lds + to * kStage + PS::kBytes, it + S::ST - 1);
-    const uint32_t at = lds + cur * kStage;
-#pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
-      bf16x8 p[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        p[u] = PS::KC ? read_frag(at + pb[sub] + (u / 2) * 4096 + (u % 2) * 512)
-                      : read_frag_tr<kPRow>(at + pb[u / 2] + sub * 32 * kPRow + (u % 2) * 8);
-#pragma unroll
-      for (int a = 0; a < MREP; ++a) {
-        const bf16x8 qa =
-            QS::KC ? read_frag(at + qb[sub] + a * 4096)
-                   : read_frag_tr<kQRow>(at + qb[a & 1] + sub * 32 * kQRow + (a >> 1) * 128);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          acc[a][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p[u], qa, acc[a][u], 0, 0, 0);
-      }
+  bf16x8 p[2][S::NR], q[MREP];
+  // one of the NR + MREP fragments of half `sub`, in the order of use
+  auto read = [&](auto sub, auto i) {
+    if constexpr (i == 0)
+      q[0] = QS::template read<0, kStep, sub>(qat);
+    else if constexpr (i <= S::NR)
+      p[sub][i - 1] = PS::template read<i - 1, 16, sub>(pat);
+    else
+      q[i - S::NR] = QS::template read<i - S::NR, kStep, sub>(qat);
+  };
+  // Reads after group a of a half whose first FROM groups read nothing: one row fragment for each
+  // group passed, and P's fragments with the first.
+  auto read_after = [&](auto sub, auto a, auto from) {
+    if constexpr (a == from - 1 || (from == 0 && a == 0)) {
+      static_for<S::NR + 1 + a>([&](auto i) { read(sub, i); });
+    } else if constexpr (a >= from) {
+      read(sub, std::integral_constant<int, a + S::NR>{});
     }
-    cur = cur == S::ST - 1 ? 0 : cur + 1;
-  }
-  // loads still under way write zeros to LDS: they end before it is used again
-  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+  };
+  auto group = [&](auto sub, auto a) {
+#pragma unroll
+    for (int u = 0; u < S::NR; ++u)
+      acc[a][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p[sub][u], q[a], acc[a][u], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr std::integral_constant<int, 0> kFirst{};
+  constexpr std::integral_constant<int, 1> kSecond{};
+  stage_ready<(S::ST - 1) * kLoads>();
+  move_to(0);
+  static_for<S::NR + MREP>([&](auto i) { read(kFirst, i); });
+  int cur = 0, it = 0;
+  auto step = [&](auto whole) {
+    static_for<MREP>([&](auto a) {
+      group(kFirst, a);
+      read_after(kSecond, a, std::integral_constant<int, 0>{});
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    const int nxt = cur == S::ST - 1 ? 0 : cur + 1;
+    i32x4 pr, qr;
+    static_for<MREP>([&](auto a) {
+      group(kSecond, a);
+      if constexpr (a == kHead - 1) {
+        move_to(nxt);
+        pr = P.template stage_resource<whole>(it + S::ST);
+        qr = Q.template stage_resource<whole>(it + S::ST);
+        stage_ready<(S::ST - 2) * kLoads>();
+      }
+      read_after(kFirst, a, std::integral_constant<int, kHead>{});
+      static_for<kLoads>([&](auto j) {
+        constexpr int at = kHead - 1 + j * (MREP - kHead + 1) / kLoads;
+        if constexpr (a == at) load(j, whole, cur, it + S::ST, pr, qr);
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    cur = nxt;
+    ++it;
+  };
+  const int fast = min(P.whole, Q.whole) - S::ST;
+  while (it < fast) step(std::integral_constant<bool, true>{});
+  while (it < n) step(kChecked);
+  // Loads still under way write zeros to LDS, and other waves may still read it: both end before it
+  // is used again.
+  stage_ready<0>();
 }
 
 __device__ __forceinline__ u32x4 pack8(f32x4 a, f32x4 b) {
@@ -438,14 +556,60 @@ __device__ __forceinline__ f32x4 act4(f32x4 v, int act) {
   return v;
 }
 
-// The position of this lane's 8 values of pair p, and its row of fragment a, in the tile.
-template <typename S>
-__device__ __forceinline__ int lane_n(int p) {
-  return wave_id() / S::WM * 64 + p * 32 + lane_id() / 16 * 8;
-}
-template <typename S>
-__device__ __forceinline__ int lane_m(int a) {
-  return (a * S::WM + wave_id() % S::WM) * 16 + lane_id() % 16;
+// f(m, n, v) with the sums of 8 consecutive positions from tile position n of tile row m on in v[0],
+// v[1]; GATED: n is the column among the tile's gate columns, v[2], v[3] the same columns' up.  Rows
+// from `rows` on are left out.
+//
+// The sums go through LDS, which the product no longer needs, 4 row fragments of a wave at a time,
+// each wave through a part of its own: what follows is then one loop over rows, whole rows of a wave
+// (256 bytes of bf16) leave together, and an activation's code is there once and not for each of 256
+// registers.  It costs 2 us of a 256 x 256 tile's 60 to 200 us.  Chunk c (16 bytes) of row r sits in
+// slot c ^ (r & 15), so that the 16 rows that one write serves differ in their banks.
+template <typename S, bool GATED, int MREP, typename F>
+__device__ __forceinline__ void each_row(const f32x4 (&acc)[MREP][S::NR], uint8_t* smem, int rows,
+                                         F f) {
+  constexpr int kFrags = MREP < 4 ? MREP : 4;
+  constexpr int kRowBytes = S::kWaveN * 4, kPart = kFrags * 16 * kRowBytes;
+  constexpr int kLanes = S::kWaveN / (GATED ? 16 : 8);  // lanes of one row
+  const int w = wave_id(), wm = w % S::WM, wn = w / S::WM, l = lane_id();
+  uint8_t* part = smem + w * kPart;
+  auto chunk = [&](int r, int c) {
+    return reinterpret_cast<f32x4*>(part + r * kRowBytes + ((c ^ (r & 15)) * 16));
+  };
+  static_for<MREP / kFrags>([&](auto pass) {
+    static_for<kFrags>([&](auto a) {
+      static_for<S::NR>([&](auto u) {
+        *chunk(a * 16 + l % 16, u * 4 + l / 16) = acc[pass * kFrags + a][u];
+      });
+    });
+    // 4 rows a lane at a time, so that their reads are under way together
+    constexpr int kRows = kWave / kLanes, kBatch = kFrags * 16 / kRows < 4 ? kFrags * 16 / kRows : 4;
+    const int j = l % kLanes;
+#pragma unroll 1
+    for (int r0 = l / kLanes; r0 < kFrags * 16; r0 += kRows * kBatch) {
+      f32x4 v[kBatch][GATED ? 4 : 2];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int r = r0 + b * kRows;
+        if constexpr (GATED) {
+          const int c = (j / 4) * 16 + (j % 4) * 2;  // 32 gate columns, then the same 32 up columns
+          v[b][0] = *chunk(r, c);
+          v[b][1] = *chunk(r, c + 1);
+          v[b][2] = *chunk(r, c + 8);
+          v[b][3] = *chunk(r, c + 9);
+        } else {
+          v[b][0] = *chunk(r, j * 2);
+          v[b][1] = *chunk(r, j * 2 + 1);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int r = r0 + b * kRows;
+        const int m = ((pass * kFrags + r / 16) * S::WM + wm) * 16 + r % 16;
+        if (m < rows) f(m, wn * (GATED ? S::kWaveN / 2 : S::kWaveN) + j * 8, v[b]);
+      }
+    }
+  });
 }
 
 // f<MREP>() with the fewest row fragments (a power of two) that cover `rows`: a tile at the end
@@ -464,7 +628,7 @@ __device__ __forceinline__ void by_height(int rows, F f) {
 
 template <typename S, bool PKC, bool QKC>
 constexpr int lds_bytes() {
-  return S::ST * (Side<PKC, true, S::BN, S::W>::kBytes + Side<QKC, false, S::BM, S::W>::kBytes);
+  return S::ST * (Side<PKC, S::BN, S::W>::kBytes + Side<QKC, S::BM, S::W>::kBytes);
 }
 
 // h = act(x Wg^T) * (x Wu^T): each wave's 64 positions are 32 gate columns and the same 32 up
@@ -481,27 +645,25 @@ __global__ __launch_bounds__(S::kThreads) void gated_kernel(
     if (t.e < 0) return;
     const int n0 = t.nt * kCols;
     const uint16_t* we = w + (int64_t(t.e) * 2 * I + n0) * H;
-    Side<true, true, S::BN, S::W> P;
-    Side<true, false, S::BM, S::W> Q;
-    P.template init<true>(we, we + int64_t(I) * H, H, H, I - n0);
+    Side<true, S::BN, S::W, true> P;
+    Side<true, S::BM, S::W> Q;
+    P.init_kc(we, we + int64_t(I) * H, H, H, I - n0);
     const uint16_t* xe = x + t.row0 * H;
-    Q.template init<false>(xe, xe, H, H, t.rows);
+    Q.init_kc(xe, xe, H, H, t.rows);
     by_height<S>(t.rows, [&](auto mrep) {
       constexpr int M = decltype(mrep)::value;
-      f32x4 acc[M][4];
+      f32x4 acc[M][S::NR];
       product<S, M>(acc, smem, P, Q, H);
-      const int n = n0 + wave_id() / S::WM * 32 + lane_id() / 16 * 8;
-#pragma unroll
-      for (int a = 0; a < M; ++a) {
-        const int m = lane_m<S>(a);
-        if (m >= t.rows || n >= I) continue;
+      each_row<S, true>(acc, smem, t.rows, [&](int m, int c, const f32x4(&v)[4]) {
+        const int n = n0 + c;
+        if (n >= I) return;
         const int64_t row = t.row0 + m;
-        store8(h + row * I + n, act4(acc[a][0], act) * acc[a][2], act4(acc[a][1], act) * acc[a][3]);
+        store8(h + row * I + n, act4(v[0], act) * v[2], act4(v[1], act) * v[3]);
         if (gu != nullptr) {
-          store8(gu + row * 2 * I + n, acc[a][0], acc[a][1]);
-          store8(gu + row * 2 * I + I + n, acc[a][2], acc[a][3]);
+          store8(gu + row * 2 * I + n, v[0], v[1]);
+          store8(gu + row * 2 * I + I + n, v[2], v[3]);
         }
-      }
+      });
     });
   }
 }
@@ -519,38 +681,34 @@ __global__ __launch_bounds__(S::kThreads) void matmul_kernel(
     const int n0 = t.nt * S::BN;
     const uint16_t* we = w + (int64_t(t.e) * N + n0) * K;
     const uint16_t* xe = x + t.row0 * K;
-    Side<true, true, S::BN, S::W> P;
-    Side<true, false, S::BM, S::W> Q;
-    P.template init<false>(we, we, K, K, N - n0);
-    Q.template init<false>(xe, xe, K, K, t.rows);
+    Side<true, S::BN, S::W> P;
+    Side<true, S::BM, S::W> Q;
+    P.init_kc(we, we, K, K, N - n0);
+    Q.init_kc(xe, xe, K, K, t.rows);
     by_height<S>(t.rows, [&](auto mrep) {
       constexpr int M = decltype(mrep)::value;
-      f32x4 acc[M][4];
+      f32x4 acc[M][S::NR];
       product<S, M>(acc, smem, P, Q, K);
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int n = n0 + lane_n<S>(p);
-        if (n >= N) continue;
-        f32x4 b0 = {0.f, 0.f, 0.f, 0.f}, b1 = b0;
-        if (bias != nullptr) load8(bias + int64_t(t.e) * N + n, b0, b1);
-#pragma unroll
-        for (int a = 0; a < M; ++a) {
-          const int m = lane_m<S>(a);
-          if (m >= t.rows) continue;
-          const int64_t at = (t.row0 + m) * N + n;
-          f32x4 v0 = acc[a][2 * p] + b0, v1 = acc[a][2 * p + 1] + b1;
-          if (pre != nullptr) store8(pre + at, v0, v1);
-          v0 = act4(v0, act);
-          v1 = act4(v1, act);
-          if (res != nullptr) {
-            f32x4 r0, r1;
-            load8(res + at, r0, r1);
-            v0 += r0;
-            v1 += r1;
-          }
-          store8(y + at, v0, v1);
+      each_row<S, false>(acc, smem, t.rows, [&](int m, int c, const f32x4(&v)[2]) {
+        const int n = n0 + c;
+        if (n >= N) return;
+        const int64_t at = (t.row0 + m) * N + n;
+        f32x4 v0 = v[0], v1 = v[1], r0, r1;
+        if (bias != nullptr) {
+          load8(bias + int64_t(t.e) * N + n, r0, r1);
+          v0 += r0;
+          v1 += r1;
         }
-      }
+        if (pre != nullptr) store8(pre + at, v0, v1);
+        v0 = act4(v0, act);
+        v1 = act4(v1, act);
+        if (res != nullptr) {
+          load8(res + at, r0, r1);
+          v0 += r0;
+          v1 += r1;
+        }
+        store8(y + at, v0, v1);
+      });
     });
   }
 }
@@ -568,24 +726,17 @@ __global__ __launch_bounds__(S::kThreads) void data_grad_kernel(
     const int n0 = t.nt * S::BN;
     const uint16_t* we = w + int64_t(t.e) * N * K + n0;
     const uint16_t* de = d + t.row0 * N;
-    Side<false, true, S::BN, S::W> P;
-    Side<true, false, S::BM, S::W> Q;
-    P.template init<false>(we, we, K, N, n0);
-    Q.template init<false>(de, de, N, N, t.rows);
+    Side<false, S::BN, S::W> P;
+    Side<true, S::BM, S::W> Q;
+    P.init_mc(we, K, N, n0);
+    Q.init_kc(de, de, N, N, t.rows);
     by_height<S>(t.rows, [&](auto mrep) {
       constexpr int M = decltype(mrep)::value;
-      f32x4 acc[M][4];
+      f32x4 acc[M][S::NR];
       product<S, M>(acc, smem, P, Q, N);
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int n = n0 + lane_n<S>(p);
-#pragma unroll
-        for (int a = 0; a < M; ++a) {
-          const int m = lane_m<S>(a);
-          if (m < t.rows && n < K)
-            store8(dx + (t.row0 + m) * K + n, acc[a][2 * p], acc[a][2 * p + 1]);
-        }
-      }
+      each_row<S, false>(acc, smem, t.rows, [&](int m, int c, const f32x4(&v)[2]) {
+        if (n0 + c < K) store8(dx + (t.row0 + m) * K + n0 + c, v[0], v[1]);
+      });
     });
   }
 }
@@ -599,9 +750,8 @@ __global__ __launch_bounds__(S::kThreads) void weight_grad_kernel(
   __shared__ __align__(1024) uint8_t smem[lds_bytes<S, false, false>()];
   const int64_t nn = (N + S::BM - 1) / S::BM, nk = (K + S::BN - 1) / S::BN;
   const int64_t total = E * nn * nk;
-  for (int64_t id = blockIdx.x;; id += gridDim.x) {
+  for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
     const int64_t seq = xcd_order(id, total);
-    if (seq >= total) return;
     const int e = int(seq / (nn * nk));
     int64_t mt, ct;
     grid_order(seq - e * nn * nk, nn, nk, mt, ct);
@@ -610,30 +760,24 @@ __global__ __launch_bounds__(S::kThreads) void weight_grad_kernel(
     expert_rows(off, e, rows, lo, cnt);
     const uint16_t* xe = x + lo * K + n0;
     const uint16_t* de = d + lo * N + m0;
-    Side<false, true, S::BN, S::W> P;
-    Side<false, false, S::BM, S::W> Q;
-    P.template init<false>(xe, xe, K, cnt, n0);
-    Q.template init<false>(de, de, N, cnt, m0);
-    f32x4 acc[S::MR][4];
+    Side<false, S::BN, S::W> P;
+    Side<false, S::BM, S::W> Q;
+    P.init_mc(xe, K, cnt, n0);
+    Q.init_mc(de, N, cnt, m0);
+    f32x4 acc[S::MR][S::NR];
     product<S, S::MR>(acc, smem, P, Q, cnt);
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int n = n0 + lane_n<S>(p);
-#pragma unroll
-      for (int a = 0; a < S::MR; ++a) {
-        const int m = m0 + lane_m<S>(a);
-        if (m >= N || n >= K) continue;
-        const int64_t at = (int64_t(e) * N + m) * K + n;
-        if (F32) {
-          f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(dw) + at);
-          o[0] = acc[a][2 * p];
-          o[1] = acc[a][2 * p + 1];
-        } else {
-          store8(static_cast<uint16_t*>(dw) + at, acc[a][2 * p], acc[a][2 * p + 1]);
-        }
+    each_row<S, false>(acc, smem, N - m0, [&](int m, int c, const f32x4(&v)[2]) {
+      if (n0 + c >= K) return;
+      const int64_t at = (int64_t(e) * N + m0 + m) * K + n0 + c;
+      if (F32) {
+        f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(dw) + at);
+        o[0] = v[0];
+        o[1] = v[1];
+      } else {
+        store8(static_cast<uint16_t*>(dw) + at, v[0], v[1]);
       }
-    }
-    __syncthreads();  // every wave has read its last stage before the next tile fills it
+    });
+    __syncthreads();  // every wave has read its sums before the next tile's loads arrive
   }
 }
 
@@ -788,18 +932,16 @@ int check_sizes(int64_t rows, int32_t E, int32_t a, int32_t b, int32_t act, bool
 }
 
 // Blocks for tiles of at most `bm` rows that `rows` rows in E runs can need, `cols` to a row of
-// tiles, rounded up to what xcd_order permutes.
+// tiles.
 int64_t row_tile_blocks(int64_t rows, int32_t E, int bm, int64_t cols) {
-  const int64_t runs = rows < E ? rows : E;
-  const int64_t n = (rows / bm + runs) * cols, group = int64_t(kXcds) * kRun;
-  return (n + group - 1) / group * group;
+  return (rows / bm + (rows < E ? rows : E)) * cols;
 }
 
 // Whether the experts have too few rows each for the tall tiles.
 bool few_rows(int64_t rows, int32_t E) { return rows <= int64_t(E) * 32; }
 
-using Big = Shape<256, 256, 2, 2>;    // 128 KiB of LDS, one block of 8 waves a CU
-using Small = Shape<64, 128, 2, 4>;   // 96 KiB, 4 waves
+using Big = Shape<256, 256, 2, 4, 2>;    // 128 KiB of LDS, one block of 8 waves a CU
+using Small = Shape<64, 128, 2, 2, 4>;   // 96 KiB, 4 waves
 
 }  // namespace
 
@@ -848,9 +990,8 @@ int moe_expert_matmul(const void* x, const int32_t* expert_offsets, const void* 
 static int weight_grad(const void* d, const void* x, const int32_t* off, int64_t rows, int E,
                        int N, int K, void* dw, int dw_f32, hipStream_t s) {
   const int64_t n = int64_t(E) * ((N + Big::BM - 1) / Big::BM) * ((K + Big::BN - 1) / Big::BN);
-  const int64_t group = int64_t(kXcds) * kRun;
   return launch(dw_f32 ? weight_grad_kernel<Big, true> : weight_grad_kernel<Big, false>,
-                (n + group - 1) / group * group, Big::kThreads, s,
+                n, Big::kThreads, s,
                 static_cast<const uint16_t*>(d), static_cast<const uint16_t*>(x), off, rows, E, N,
                 K, dw);
 }
