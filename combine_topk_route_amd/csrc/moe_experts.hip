@@ -105,6 +105,22 @@ __device__ __forceinline__ void expert_rows(const int32_t* off, int e, int64_t r
   n = b - a;
 }
 
+// How the n rows of an expert are cut into tiles of at most BM rows, BM = FULL or FULL + 32: `count`
+// tiles of `height` rows, a multiple of 32 (the last may be shorter).  Tiles of FULL rows, unless these
+// leave a last one that is at most half full where FULL + 32 rows need one tile less: a short tile
+// costs far more than its share, as it waits for the same weights.  Then the rows are spread evenly.
+template <int FULL, int BM>
+__device__ __forceinline__ void cut_rows(int64_t n, int& count, int& height) {
+  int64_t c = (n + FULL - 1) / FULL;
+  const int64_t fewer = (n + BM - 1) / BM;
+  if (fewer < c && n - (c - 1) * FULL <= FULL / 2) c = fewer;
+  if (c == 0) c = 1;
+  const int64_t h = (n + c - 1) / c;
+  height = int((h + 31) / 32 * 32);
+  if (height == 0) height = 32;
+  count = int((n + height - 1) / height);
+}
+
 struct Tile {
   int e;         // expert, or -1 past the last tile
   int64_t row0;  // first row
@@ -162,13 +178,13 @@ __device__ __forceinline__ int wave_prefix(int v) {
 // The tile of block number `id`.  Every thread of the block calls it.  Each thread counts the row
 // tiles of `kPer` experts; the one that holds the tile writes it down.  At most 2^31 / 64 + 1024 row
 // tiles, so the counts fit 32 bits.
-template <int BM, int THREADS>
+template <int FULL, int BM, int THREADS>
 __device__ Tile find_tile(const int32_t* off, int E, int64_t rows, int ncol, int64_t id) {
   constexpr int kPer = kMaxE / THREADS, kWaves = THREADS / kWave;
   __shared__ int s_wave[kWaves];
   __shared__ Tile s_tile;
   int64_t lo[kPer];
-  int n[kPer], mine = 0;
+  int n[kPer], mt[kPer], height[kPer], mine = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = threadIdx.x * kPer + i;
@@ -176,7 +192,8 @@ __device__ Tile find_tile(const int32_t* off, int E, int64_t rows, int ncol, int
     lo[i] = 0;
     if (e < E) expert_rows(off, e, rows, lo[i], cnt);
     n[i] = int(cnt);
-    mine += int((cnt + BM - 1) / BM);
+    cut_rows<FULL, BM>(cnt, mt[i], height[i]);
+    mine += mt[i];
   }
   const int incl = wave_prefix(mine);
   const int w = threadIdx.x / kWave;
@@ -197,16 +214,16 @@ __device__ Tile find_tile(const int32_t* off, int E, int64_t rows, int ncol, int
     if (local >= 0 && local < int64_t(mine) * ncol) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int mt = int((int64_t(n[i]) + BM - 1) / BM);
-        if (local >= 0 && local < int64_t(mt) * ncol) {
+        if (local >= 0 && local < int64_t(mt[i]) * ncol) {
           int64_t m, c;
-          grid_order(local, mt, ncol, m, c);
+          grid_order(local, mt[i], ncol, m, c);
+          const int64_t left = n[i] - m * height[i];
           s_tile.e = threadIdx.x * kPer + i;
-          s_tile.row0 = lo[i] + m * BM;
-          s_tile.rows = int(n[i] - m * BM < BM ? n[i] - m * BM : BM);
+          s_tile.row0 = lo[i] + m * height[i];
+          s_tile.rows = int(left < height[i] ? left : height[i]);
           s_tile.nt = int(c);
         }
-        local -= int64_t(mt) * ncol;
+        local -= int64_t(mt[i]) * ncol;
       }
     }
   }
@@ -405,14 +422,20 @@ __device__ __forceinline__ void static_for(F f) {
   }
 }
 
-// The tile shape: BM x BN outputs by WM x WN waves, each (BM / WM) x 64, ST stages in LDS.
-// A wave's row fragment i covers rows 16 (i * WM + wave row), so that a short tile loads every
-// wave alike.
-template <int BM_, int BN_, int WM_, int WN_, int ST_>
+// The tile shape: up to BM x BN outputs (rows are cut by FULL, see cut_rows) by WM x WN waves.  A wave's
+// row fragment i covers rows 16 (i * WM + wave row), so that a short tile loads every wave alike.
+template <int FULL_, int BM_, int BN_, int WM_, int WN_, int LDS_>
 struct Shape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_;
+  static constexpr int FULL = FULL_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, kLds = LDS_;
   static constexpr int W = WM * WN, kThreads = W * kWave;
   static constexpr int kWaveN = BN / WN, MR = BM / WM / 16, NR = kWaveN / 16;
+  // Rows that one load of every wave brings, and the rows a stage holds for MREP row fragments.
+  static constexpr int kLoadRows = W * 8;
+  template <int MREP>
+  static constexpr int kRows = (MREP * 16 * WM + kLoadRows - 1) / kLoadRows * kLoadRows;
+  // As many stages as fit, 4 at most.
+  template <int BYTES>
+  static constexpr int kStages = kLds / BYTES < 4 ? kLds / BYTES : 4;
 };
 
 // A value that the compiler takes as it finds it: what is added to it stays in the offsets of the
@@ -439,7 +462,8 @@ __device__ __forceinline__ int opaque_scalar(int v) {
 template <typename S, int MREP, typename PS, typename QS>
 __device__ __forceinline__ void product(f32x4 (&acc)[MREP][S::NR], uint8_t* smem, const PS& P,
                                         const QS& Q, int64_t K) {
-  constexpr int kStage = PS::kBytes + QS::kBytes;
+  constexpr int kStage = PS::kBytes + QS::kBytes, ST = S::template kStages<kStage>;
+  static_assert(ST >= 2, "one stage is computed while the next arrives");
   constexpr int kLoads = PS::kLoads + QS::kLoads;
   constexpr int kHead = MREP >= 4 ? 2 : 1, kStep = 16 * S::WM;
   const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_address(smem));
@@ -468,7 +492,7 @@ __device__ __forceinline__ void product(f32x4 (&acc)[MREP][S::NR], uint8_t* smem
   };
   constexpr std::integral_constant<bool, false> kChecked{};
 #pragma unroll
-  for (int st = 0; st < S::ST; ++st) {
+  for (int st = 0; st < ST; ++st) {
     const i32x4 pr = P.template stage_resource<false>(st), qr = Q.template stage_resource<false>(st);
     static_for<kLoads>([&](auto j) { load(j, kChecked, st, st, pr, qr); });
   }
@@ -499,7 +523,7 @@ __device__ __forceinline__ void product(f32x4 (&acc)[MREP][S::NR], uint8_t* smem
   };
   constexpr std::integral_constant<int, 0> kFirst{};
   constexpr std::integral_constant<int, 1> kSecond{};
-  stage_ready<(S::ST - 1) * kLoads>();
+  stage_ready<(ST - 1) * kLoads>();
   move_to(0);
   static_for<S::NR + MREP>([&](auto i) { read(kFirst, i); });
   int cur = 0, it = 0;
@@ -509,27 +533,27 @@ __device__ __forceinline__ void product(f32x4 (&acc)[MREP][S::NR], uint8_t* smem
       read_after(kSecond, a, std::integral_constant<int, 0>{});
       __builtin_amdgcn_sched_barrier(0);
     });
-    const int nxt = cur == S::ST - 1 ? 0 : cur + 1;
+    const int nxt = cur == ST - 1 ? 0 : cur + 1;
     i32x4 pr, qr;
     static_for<MREP>([&](auto a) {
       group(kSecond, a);
       if constexpr (a == kHead - 1) {
         move_to(nxt);
-        pr = P.template stage_resource<whole>(it + S::ST);
-        qr = Q.template stage_resource<whole>(it + S::ST);
-        stage_ready<(S::ST - 2) * kLoads>();
+        pr = P.template stage_resource<whole>(it + ST);
+        qr = Q.template stage_resource<whole>(it + ST);
+        stage_ready<(ST - 2) * kLoads>();
       }
       read_after(kFirst, a, std::integral_constant<int, kHead>{});
       static_for<kLoads>([&](auto j) {
         constexpr int at = kHead - 1 + j * (MREP - kHead + 1) / kLoads;
-        if constexpr (a == at) load(j, whole, cur, it + S::ST, pr, qr);
+        if constexpr (a == at) load(j, whole, cur, it + ST, pr, qr);
       });
       __builtin_amdgcn_sched_barrier(0);
     });
     cur = nxt;
     ++it;
   };
-  const int fast = min(P.whole, Q.whole) - S::ST;
+  const int fast = min(P.whole, Q.whole) - ST;
   while (it < fast) step(std::integral_constant<bool, true>{});
   while (it < n) step(kChecked);
   // Loads still under way write zeros to LDS, and other waves may still read it: both end before it
@@ -568,7 +592,8 @@ __device__ __forceinline__ f32x4 act4(f32x4 v, int act) {
 template <typename S, bool GATED, int MREP, typename F>
 __device__ __forceinline__ void each_row(const f32x4 (&acc)[MREP][S::NR], uint8_t* smem, int rows,
                                          F f) {
-  constexpr int kFrags = MREP < 4 ? MREP : 4;
+  constexpr int kFrags = MREP <= 4 ? MREP : MREP % 3 == 0 ? 3 : 4;
+  static_assert(MREP % kFrags == 0, "");
   constexpr int kRowBytes = S::kWaveN * 4, kPart = kFrags * 16 * kRowBytes;
   constexpr int kLanes = S::kWaveN / (GATED ? 16 : 8);  // lanes of one row
   const int w = wave_id(), wm = w % S::WM, wn = w / S::WM, l = lane_id();
@@ -582,8 +607,10 @@ __device__ __forceinline__ void each_row(const f32x4 (&acc)[MREP][S::NR], uint8_
         *chunk(a * 16 + l % 16, u * 4 + l / 16) = acc[pass * kFrags + a][u];
       });
     });
-    // 4 rows a lane at a time, so that their reads are under way together
-    constexpr int kRows = kWave / kLanes, kBatch = kFrags * 16 / kRows < 4 ? kFrags * 16 / kRows : 4;
+    // a few rows a lane at a time, so that their reads are under way together
+    constexpr int kRows = kWave / kLanes, kSteps = kFrags * 16 / kRows;
+    constexpr int kBatch = kSteps % 4 == 0 ? 4 : kSteps % 3 == 0 ? 3 : kSteps;
+    static_assert(kSteps % kBatch == 0 && kBatch <= 4, "rows of a pass in whole batches");
     const int j = l % kLanes;
 #pragma unroll 1
     for (int r0 = l / kLanes; r0 < kFrags * 16; r0 += kRows * kBatch) {
@@ -612,23 +639,21 @@ __device__ __forceinline__ void each_row(const f32x4 (&acc)[MREP][S::NR], uint8_
   });
 }
 
-// f<MREP>() with the fewest row fragments (a power of two) that cover `rows`: a tile at the end
-// of an expert computes no more than twice its rows.
+// f<MREP>() with the fewest row fragments out of a few choices that cover `rows`.
 template <typename S, typename F>
 __device__ __forceinline__ void by_height(int rows, F f) {
   const int need = (rows + 16 * S::WM - 1) / (16 * S::WM);
+  if constexpr (S::MR >= 9)
+    if (need > 8) return f(std::integral_constant<int, 9>{});
   if constexpr (S::MR >= 8)
-    if (need > 4) return f(std::integral_constant<int, 8>{});
+    if (need > 6) return f(std::integral_constant<int, 8>{});
+  if constexpr (S::MR >= 6)
+    if (need > 4) return f(std::integral_constant<int, 6>{});
   if constexpr (S::MR >= 4)
     if (need > 2) return f(std::integral_constant<int, 4>{});
   if constexpr (S::MR >= 2)
     if (need > 1) return f(std::integral_constant<int, 2>{});
   f(std::integral_constant<int, 1>{});
-}
-
-template <typename S, bool PKC, bool QKC>
-constexpr int lds_bytes() {
-  return S::ST * (Side<PKC, S::BN, S::W>::kBytes + Side<QKC, S::BM, S::W>::kBytes);
 }
 
 // h = act(x Wg^T) * (x Wu^T): each wave's 64 positions are 32 gate columns and the same 32 up
@@ -637,21 +662,21 @@ template <typename S>
 __global__ __launch_bounds__(S::kThreads) void gated_kernel(
     const uint16_t* x, const int32_t* off, const uint16_t* w, int64_t rows, int E, int H, int I,
     int act, uint16_t* h, uint16_t* gu) {
-  __shared__ __align__(1024) uint8_t smem[lds_bytes<S, true, true>()];
+  __shared__ __align__(1024) uint8_t smem[S::kLds];
   constexpr int kCols = S::BN / 2;
   const int ncol = (I + kCols - 1) / kCols;
   for (int64_t id = blockIdx.x;; id += gridDim.x) {
-    const Tile t = find_tile<S::BM, S::kThreads>(off, E, rows, ncol, id);
+    const Tile t = find_tile<S::FULL, S::BM, S::kThreads>(off, E, rows, ncol, id);
     if (t.e < 0) return;
     const int n0 = t.nt * kCols;
     const uint16_t* we = w + (int64_t(t.e) * 2 * I + n0) * H;
     Side<true, S::BN, S::W, true> P;
-    Side<true, S::BM, S::W> Q;
     P.init_kc(we, we + int64_t(I) * H, H, H, I - n0);
     const uint16_t* xe = x + t.row0 * H;
-    Q.init_kc(xe, xe, H, H, t.rows);
     by_height<S>(t.rows, [&](auto mrep) {
       constexpr int M = decltype(mrep)::value;
+      Side<true, S::template kRows<M>, S::W> Q;
+      Q.init_kc(xe, xe, H, H, t.rows);
       f32x4 acc[M][S::NR];
       product<S, M>(acc, smem, P, Q, H);
       each_row<S, true>(acc, smem, t.rows, [&](int m, int c, const f32x4(&v)[4]) {
@@ -673,20 +698,20 @@ template <typename S>
 __global__ __launch_bounds__(S::kThreads) void matmul_kernel(
     const uint16_t* x, const int32_t* off, const uint16_t* w, const uint16_t* bias,
     const uint16_t* res, int64_t rows, int E, int K, int N, int act, uint16_t* y, uint16_t* pre) {
-  __shared__ __align__(1024) uint8_t smem[lds_bytes<S, true, true>()];
+  __shared__ __align__(1024) uint8_t smem[S::kLds];
   const int ncol = (N + S::BN - 1) / S::BN;
   for (int64_t id = blockIdx.x;; id += gridDim.x) {
-    const Tile t = find_tile<S::BM, S::kThreads>(off, E, rows, ncol, id);
+    const Tile t = find_tile<S::FULL, S::BM, S::kThreads>(off, E, rows, ncol, id);
     if (t.e < 0) return;
     const int n0 = t.nt * S::BN;
     const uint16_t* we = w + (int64_t(t.e) * N + n0) * K;
     const uint16_t* xe = x + t.row0 * K;
     Side<true, S::BN, S::W> P;
-    Side<true, S::BM, S::W> Q;
     P.init_kc(we, we, K, K, N - n0);
-    Q.init_kc(xe, xe, K, K, t.rows);
     by_height<S>(t.rows, [&](auto mrep) {
       constexpr int M = decltype(mrep)::value;
+      Side<true, S::template kRows<M>, S::W> Q;
+      Q.init_kc(xe, xe, K, K, t.rows);
       f32x4 acc[M][S::NR];
       product<S, M>(acc, smem, P, Q, K);
       each_row<S, false>(acc, smem, t.rows, [&](int m, int c, const f32x4(&v)[2]) {
@@ -718,20 +743,20 @@ template <typename S>
 __global__ __launch_bounds__(S::kThreads) void data_grad_kernel(
     const uint16_t* d, const int32_t* off, const uint16_t* w, int64_t rows, int E, int N, int K,
     uint16_t* dx) {
-  __shared__ __align__(1024) uint8_t smem[lds_bytes<S, false, true>()];
+  __shared__ __align__(1024) uint8_t smem[S::kLds];
   const int ncol = (K + S::BN - 1) / S::BN;
   for (int64_t id = blockIdx.x;; id += gridDim.x) {
-    const Tile t = find_tile<S::BM, S::kThreads>(off, E, rows, ncol, id);
+    const Tile t = find_tile<S::FULL, S::BM, S::kThreads>(off, E, rows, ncol, id);
     if (t.e < 0) return;
     const int n0 = t.nt * S::BN;
     const uint16_t* we = w + int64_t(t.e) * N * K + n0;
     const uint16_t* de = d + t.row0 * N;
     Side<false, S::BN, S::W> P;
-    Side<true, S::BM, S::W> Q;
     P.init_mc(we, K, N, n0);
-    Q.init_kc(de, de, N, N, t.rows);
     by_height<S>(t.rows, [&](auto mrep) {
       constexpr int M = decltype(mrep)::value;
+      Side<true, S::template kRows<M>, S::W> Q;
+      Q.init_kc(de, de, N, N, t.rows);
       f32x4 acc[M][S::NR];
       product<S, M>(acc, smem, P, Q, N);
       each_row<S, false>(acc, smem, t.rows, [&](int m, int c, const f32x4(&v)[2]) {
@@ -747,7 +772,7 @@ template <typename S, bool F32>
 __global__ __launch_bounds__(S::kThreads) void weight_grad_kernel(
     const uint16_t* d, const uint16_t* x, const int32_t* off, int64_t rows, int E, int N, int K,
     void* dw) {
-  __shared__ __align__(1024) uint8_t smem[lds_bytes<S, false, false>()];
+  __shared__ __align__(1024) uint8_t smem[S::kLds];
   const int64_t nn = (N + S::BM - 1) / S::BM, nk = (K + S::BN - 1) / S::BN;
   const int64_t total = E * nn * nk;
   for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
@@ -940,8 +965,10 @@ int64_t row_tile_blocks(int64_t rows, int32_t E, int bm, int64_t cols) {
 // Whether the experts have too few rows each for the tall tiles.
 bool few_rows(int64_t rows, int32_t E) { return rows <= int64_t(E) * 32; }
 
-using Big = Shape<256, 256, 2, 4, 2>;    // 128 KiB of LDS, one block of 8 waves a CU
-using Small = Shape<64, 128, 2, 2, 4>;   // 96 KiB, 4 waves
+// One block of 8 waves a CU: two stages of 32 KiB of weights and up to 40 KiB of rows.
+using Tall = Shape<256, 288, 256, 2, 4, 144 * 1024>;
+using Square = Shape<256, 256, 256, 2, 4, 128 * 1024>;
+using Small = Shape<64, 64, 128, 2, 2, 96 * 1024>;  // 4 waves
 
 }  // namespace
 
@@ -958,13 +985,13 @@ int moe_expert_gated(const void* x, const int32_t* expert_offsets, const void* w
     return MOE_ERR_ALIGNMENT;
   auto run = [&](auto shape, auto kern) {
     using S = decltype(shape);
-    return launch(kern, row_tile_blocks(rows, E, S::BM, (I + S::BN / 2 - 1) / (S::BN / 2)),
+    return launch(kern, row_tile_blocks(rows, E, S::FULL, (I + S::BN / 2 - 1) / (S::BN / 2)),
                   S::kThreads, static_cast<hipStream_t>(stream),
                   static_cast<const uint16_t*>(x), expert_offsets,
                   static_cast<const uint16_t*>(w_gate_up), rows, E, H, I, act,
                   static_cast<uint16_t*>(h), static_cast<uint16_t*>(gate_up));
   };
-  return few_rows(rows, E) ? run(Small{}, gated_kernel<Small>) : run(Big{}, gated_kernel<Big>);
+  return few_rows(rows, E) ? run(Small{}, gated_kernel<Small>) : run(Tall{}, gated_kernel<Tall>);
 }
 
 int moe_expert_matmul(const void* x, const int32_t* expert_offsets, const void* w,
@@ -978,28 +1005,28 @@ int moe_expert_matmul(const void* x, const int32_t* expert_offsets, const void* 
     return MOE_ERR_ALIGNMENT;
   auto run = [&](auto shape, auto kern) {
     using S = decltype(shape);
-    return launch(kern, row_tile_blocks(rows, E, S::BM, (N + S::BN - 1) / S::BN), S::kThreads,
+    return launch(kern, row_tile_blocks(rows, E, S::FULL, (N + S::BN - 1) / S::BN), S::kThreads,
                   static_cast<hipStream_t>(stream), static_cast<const uint16_t*>(x),
                   expert_offsets, static_cast<const uint16_t*>(w),
                   static_cast<const uint16_t*>(bias), static_cast<const uint16_t*>(residual), rows,
                   E, K, N, act, static_cast<uint16_t*>(y), static_cast<uint16_t*>(pre));
   };
-  return few_rows(rows, E) ? run(Small{}, matmul_kernel<Small>) : run(Big{}, matmul_kernel<Big>);
+  return few_rows(rows, E) ? run(Small{}, matmul_kernel<Small>) : run(Tall{}, matmul_kernel<Tall>);
 }
 
 static int weight_grad(const void* d, const void* x, const int32_t* off, int64_t rows, int E,
                        int N, int K, void* dw, int dw_f32, hipStream_t s) {
-  const int64_t n = int64_t(E) * ((N + Big::BM - 1) / Big::BM) * ((K + Big::BN - 1) / Big::BN);
-  return launch(dw_f32 ? weight_grad_kernel<Big, true> : weight_grad_kernel<Big, false>,
-                n, Big::kThreads, s,
+  const int64_t n = int64_t(E) * ((N + Square::BM - 1) / Square::BM) * ((K + Square::BN - 1) / Square::BN);
+  return launch(dw_f32 ? weight_grad_kernel<Square, true> : weight_grad_kernel<Square, false>,
+                n, Square::kThreads, s,
                 static_cast<const uint16_t*>(d), static_cast<const uint16_t*>(x), off, rows, E, N,
                 K, dw);
 }
 
 static int data_grad(const void* d, const int32_t* off, const void* w, int64_t rows, int E, int N,
                      int K, void* dx, hipStream_t s) {
-  return launch(data_grad_kernel<Big>,
-                row_tile_blocks(rows, E, Big::BM, (K + Big::BN - 1) / Big::BN), Big::kThreads, s,
+  return launch(data_grad_kernel<Tall>,
+                row_tile_blocks(rows, E, Tall::FULL, (K + Tall::BN - 1) / Tall::BN), Tall::kThreads, s,
                 static_cast<const uint16_t*>(d), off, static_cast<const uint16_t*>(w), rows, E, N,
                 K, static_cast<uint16_t*>(dx));
 }
