@@ -16,12 +16,14 @@ import torch
 
 from . import _lib
 from . import binding as _b
+from . import experts as _e
 
 
 class MoeBuffers:
     """Preallocated outputs and workspace for batches of up to ``max_tokens``.
 
-    ``num_vranks`` virtual ranks own ``E // num_vranks`` experts each; the
+    ``intermediate`` adds what ``experts`` needs for an inner size of so many
+    features.  ``num_vranks`` virtual ranks own ``E // num_vranks`` experts each; the
     dispatch buffer has capacity ``max_tokens * k`` rows (no drops).  Methods
     return views of the buffers sized to the batch; the views are overwritten
     by the next call.
@@ -29,7 +31,7 @@ class MoeBuffers:
 
     def __init__(self, max_tokens: int, hidden: int, num_experts: int, k: int,
                  num_vranks: int = 1, device: Optional[torch.device] = None,
-                 fp8: bool = False):
+                 fp8: bool = False, intermediate: Optional[int] = None):
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
         self.max_tokens, self.H, self.E, self.k, self.R = max_tokens, hidden, num_experts, k, num_vranks
         self.device_index = dev.index if dev.index is not None else torch.cuda.current_device()
@@ -54,6 +56,11 @@ class MoeBuffers:
         if fp8:
             self.buf_q = torch.empty((cap, hidden), dtype=torch.uint8, device=dev)
             self.buf_scale = torch.empty((cap, hidden // 128), dtype=f32, device=dev)
+        # The experts' inner rows and their outputs, for `experts`.
+        self.h = self.y = None
+        if intermediate is not None:
+            self.h = torch.empty((cap, intermediate), dtype=torch.bfloat16, device=dev)
+            self.y = torch.empty((cap, hidden), dtype=torch.bfloat16, device=dev)
         self._views = None
 
     def _t(self, T: int) -> int:
@@ -140,6 +147,20 @@ class MoeBuffers:
             lp, xp, T, self.E, self.k, n_group, topk_group, self.H, self.R,
             *v.route_dispatch_fp8_args, _b._stream(stream, x)))
         return v.topk_idx, v.topk_w, v.send, v.buf_q, v.buf_scale
+
+    def experts(self, x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor,
+                act: str = "silu", stream=None) -> torch.Tensor:
+        """The experts on the rows of the last dispatch (x [T*k, H], as dispatch
+        returns them): the gated block and the product back to the hidden size.
+        Returns y [T*k, H], as combine takes it."""
+        if self.h is None:
+            raise ValueError("constructed without intermediate=")
+        if x.dim() != 2 or x.shape[0] > self.h.shape[0]:
+            raise ValueError(f"x must be [at most {self.h.shape[0]}, {self.H}]")
+        h, y = self.h[: x.shape[0]], self.y[: x.shape[0]]
+        _e.moe_expert_gated(x, self.expert_offsets, w_gate_up, act, h=h, stream=stream)
+        _e.moe_expert_matmul(h, self.expert_offsets, w_down, y=y, stream=stream)
+        return y
 
     def combine(self, y: torch.Tensor, pair_row: torch.Tensor, topk_w: torch.Tensor,
                 stream=None) -> torch.Tensor:

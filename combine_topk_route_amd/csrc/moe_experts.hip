@@ -37,6 +37,8 @@ constexpr int kMaxK = 32;
 constexpr int64_t kMaxPairs = (int64_t(1) << 31) - 1;
 constexpr int kMaxFeatures = 1 << 20;
 constexpr int64_t kMaxBlocks = int64_t(1) << 20;  // blocks loop over tiles past this
+constexpr int64_t kMaxTiles = (int64_t(1) << 31) - 1;
+constexpr int kCus = 256;  // blocks of a kernel that goes through its tiles in one sequence
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -59,18 +61,44 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // activations
 // ---------------------------------------------------------------------------
 
-// 1 / (1 + exp(-z)); exp overflows to infinity for z < -88, which gives 0.
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
+// They run on every value of a product's tile, so they are built on the hardware's exp2 and reciprocal
+// (1 ulp each).  The argument of exp2 is rounded in fp32, so the relative error grows with |z|, to
+// 2^-18 |z| at most: far below half a step of bf16, as which the result is stored.
 
-constexpr float kInvSqrt2 = 0.70710678118654752f;
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 
-// z * Phi(z) through erfc, which keeps its relative precision in the left tail
-// where 1 + erf cancels.
+// 1 / (1 + exp(-z)); exp2 overflows to infinity for z < -88, which gives 0.
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * z));
+}
+
+// Phi(z), the normal distribution function, and exp(-z^2 / 2).  The tail Phi(-x), x >= 0, is
+// exp(-x^2 / 2) t P(t) with t = 1 / (1 + 0.3 x): the factor t P(t) falls like 1 / x and is smooth in
+// t, so that P of degree 7, fitted here to a least largest relative error over 0 <= x <= 14, holds it
+// to 1.5e-7 (4.7e-7 evaluated in fp32).  The left tail keeps its relative precision, where 1 + erf
+// would cancel.
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+  const float x = __builtin_fabsf(z);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3f, x, 1.0f));
+  e = __builtin_amdgcn_exp2f(-0.5f * kLog2e * (z * z));
+  float p = 0.0356763f;
+  p = __builtin_fmaf(p, t, -0.15720925f);
+  p = __builtin_fmaf(p, t, 0.20636382f);
+  p = __builtin_fmaf(p, t, -0.05369288f);
+  p = __builtin_fmaf(p, t, 0.12856639f);
+  p = __builtin_fmaf(p, t, 0.09991208f);
+  p = __builtin_fmaf(p, t, 0.12075418f);
+  p = __builtin_fmaf(p, t, 0.11962928f);
+  const float tail = e * (p * t);
+  return z < 0.f ? tail : 1.0f - tail;
+}
+
 __device__ __forceinline__ float act_value(float z, int act) {
+  float e;
   switch (act) {
     case MOE_ACT_SILU: return z * sigmoid(z);
-    case MOE_ACT_GELU: return 0.5f * z * erfcf(-z * kInvSqrt2);
+    case MOE_ACT_GELU: return z * normal_cdf(z, e);
     case MOE_ACT_RELU: return z < 0.f ? 0.f : z;  // a NaN stays one
     default: return z;
   }
@@ -78,13 +106,16 @@ __device__ __forceinline__ float act_value(float z, int act) {
 
 // d act / dz (relu's is 0 at 0).
 __device__ __forceinline__ float act_slope(float z, int act) {
+  float e;
   switch (act) {
     case MOE_ACT_SILU: {
       const float s = sigmoid(z);
       return s * (1.f + z * (1.f - s));
     }
-    case MOE_ACT_GELU:
-      return 0.5f * erfcf(-z * kInvSqrt2) + z * expf(-0.5f * z * z) * kInvSqrt2Pi;
+    case MOE_ACT_GELU: {
+      const float phi = normal_cdf(z, e);
+      return __builtin_fmaf(z * e, kInvSqrt2Pi, phi);
+    }
     case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
     default: return 1.f;
   }
@@ -110,15 +141,37 @@ __device__ __forceinline__ void expert_rows(const int32_t* off, int e, int64_t r
 // leave a last one that is at most half full where FULL + 32 rows need one tile less: a short tile
 // costs far more than its share, as it waits for the same weights.  Then the rows are spread evenly.
 template <int FULL, int BM>
-__device__ __forceinline__ void cut_rows(int64_t n, int& count, int& height) {
-  int64_t c = (n + FULL - 1) / FULL;
-  const int64_t fewer = (n + BM - 1) / BM;
-  if (fewer < c && n - (c - 1) * FULL <= FULL / 2) c = fewer;
-  if (c == 0) c = 1;
-  const int64_t h = (n + c - 1) / c;
-  height = int((h + 31) / 32 * 32);
-  if (height == 0) height = 32;
-  count = int((n + height - 1) / height);
+__device__ __forceinline__ void cut_rows(uint32_t n, int& count, int& height) {
+  uint32_t c = (n + FULL - 1) / FULL;
+  height = FULL;
+  if (BM > FULL) {
+    const uint32_t fewer = (n + BM - 1) / BM;
+    if (fewer < c && n - (c - 1) * FULL <= FULL / 2) c = fewer;
+    const uint32_t h = c > 1 ? (n + c - 1) / c : n;
+    height = int((h + 31) / 32 * 32);
+    if (c > 1) c = (n + height - 1) / uint32_t(height);
+  }
+  count = int(c);
+}
+
+// A value every lane of the wave has, in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return int64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(v)))) |
+         int64_t(__builtin_amdgcn_readfirstlane(int(v >> 32))) << 32;
+}
+
+// The same for an expert that is the same for the whole wave: through the scalar cache, whose loads
+// are waited for apart from the vector loads and stores under way.
+__device__ __forceinline__ void expert_rows_scalar(const int32_t* off, int e, int64_t rows,
+                                                   int64_t& lo, int64_t& n) {
+  typedef const __attribute__((address_space(4))) int32_t* Scalar;
+  const Scalar o = (Scalar)(off);
+  e = __builtin_amdgcn_readfirstlane(e);
+  int64_t a = o[e], b = o[e + 1];
+  a = a < 0 ? 0 : (a > rows ? rows : a);
+  b = b < a ? a : (b > rows ? rows : b);
+  lo = a;
+  n = b - a;
 }
 
 struct Tile {
@@ -133,15 +186,15 @@ struct Tile {
 // numbers go to the XCDs in runs of 32 (its CUs), and what is left of `total`
 // after the last round of such runs in runs half as long, and so on: a bijection
 // on [0, total).  From `total` on the number is returned as it is.
-constexpr int kXcds = 8;
+constexpr uint32_t kXcds = 8;
 
-__device__ __forceinline__ int64_t xcd_order(int64_t id, int64_t total) {
-  int64_t base = 0;
+__device__ __forceinline__ uint32_t xcd_order(uint32_t id, uint32_t total) {
+  uint32_t base = 0;
 #pragma unroll
-  for (int run = 32; run >= 1; run >>= 1) {
-    const int64_t span = (total - base) / (kXcds * run) * (kXcds * run);
+  for (uint32_t run = 32; run >= 1; run >>= 1) {
+    const uint32_t span = (total - base) / (kXcds * run) * (kXcds * run);
     if (id < base + span) {
-      const int64_t i = id - base, j = i / kXcds;
+      const uint32_t i = id - base, j = i / kXcds;
       return base + (j / run * kXcds + i % kXcds) * run + j % run;
     }
     base += span;
@@ -151,12 +204,12 @@ __device__ __forceinline__ int64_t xcd_order(int64_t id, int64_t total) {
 
 // Tile `local` of a grid of mt x nt tiles: strips of 8 row tiles, inside a strip
 // the row tile first, so that 32 neighbours read 8 + 4 strips of the operands.
-__device__ __forceinline__ void grid_order(int64_t local, int64_t mt, int64_t nt, int64_t& m,
-                                           int64_t& n) {
-  const int64_t g = local / (8 * nt), rem = local - g * 8 * nt;
-  const int64_t gm = mt - g * 8 < 8 ? mt - g * 8 : 8;
-  m = g * 8 + rem % gm;
-  n = rem / gm;
+__device__ __forceinline__ void grid_order(uint32_t local, uint32_t mt, uint32_t nt, int& m,
+                                           int& n) {
+  const uint32_t g = local / (8 * nt), rem = local - g * 8 * nt;
+  const uint32_t gm = mt - g * 8 < 8 ? mt - g * 8 : 8;
+  n = int(rem / gm);
+  m = int(g * 8 + rem % gm);
 }
 
 // Inclusive prefix sum over the 64 lanes: four shifts inside each 16-lane row, then each row's total
@@ -176,10 +229,9 @@ __device__ __forceinline__ int wave_prefix(int v) {
 }
 
 // The tile of block number `id`.  Every thread of the block calls it.  Each thread counts the row
-// tiles of `kPer` experts; the one that holds the tile writes it down.  At most 2^31 / 64 + 1024 row
-// tiles, so the counts fit 32 bits.
+// tiles of `kPer` experts; the one that holds the tile writes it down.  The host refuses more than 2^31 - 1 tiles.
 template <int FULL, int BM, int THREADS>
-__device__ Tile find_tile(const int32_t* off, int E, int64_t rows, int ncol, int64_t id) {
+__device__ Tile find_tile(const int32_t* off, int E, int64_t rows, int ncol, uint32_t id) {
   constexpr int kPer = kMaxE / THREADS, kWaves = THREADS / kWave;
   __shared__ int s_wave[kWaves];
   __shared__ Tile s_tile;
@@ -192,7 +244,7 @@ __device__ Tile find_tile(const int32_t* off, int E, int64_t rows, int ncol, int
     lo[i] = 0;
     if (e < E) expert_rows(off, e, rows, lo[i], cnt);
     n[i] = int(cnt);
-    cut_rows<FULL, BM>(cnt, mt[i], height[i]);
+    cut_rows<FULL, BM>(uint32_t(cnt), mt[i], height[i]);
     mine += mt[i];
   }
   const int incl = wave_prefix(mine);
@@ -207,23 +259,22 @@ __device__ Tile find_tile(const int32_t* off, int E, int64_t rows, int ncol, int
     if (i < w) pre += v;
     total += v;
   }
-  const int64_t tiles = int64_t(__builtin_amdgcn_readfirstlane(total)) * ncol;
+  const uint32_t tiles = uint32_t(__builtin_amdgcn_readfirstlane(total)) * uint32_t(ncol);
   if (id < tiles) {
-    const int64_t seq = xcd_order(id, tiles);
-    int64_t local = seq - int64_t(pre) * ncol;
-    if (local >= 0 && local < int64_t(mine) * ncol) {
+    int local = int(xcd_order(id, tiles)) - pre * ncol;
+    if (local >= 0 && local < mine * ncol) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        if (local >= 0 && local < int64_t(mt[i]) * ncol) {
-          int64_t m, c;
+        if (local >= 0 && local < mt[i] * ncol) {
+          int m, c;
           grid_order(local, mt[i], ncol, m, c);
-          const int64_t left = n[i] - m * height[i];
+          const int left = n[i] - m * height[i];
           s_tile.e = threadIdx.x * kPer + i;
           s_tile.row0 = lo[i] + m * height[i];
-          s_tile.rows = int(left < height[i] ? left : height[i]);
-          s_tile.nt = int(c);
+          s_tile.rows = left < height[i] ? left : height[i];
+          s_tile.nt = c;
         }
-        local -= int64_t(mt[i]) * ncol;
+        local -= mt[i] * ncol;
       }
     }
   }
@@ -233,8 +284,7 @@ __device__ Tile find_tile(const int32_t* off, int E, int64_t rows, int ncol, int
   t.e = __builtin_amdgcn_readfirstlane(t.e);
   t.rows = __builtin_amdgcn_readfirstlane(t.rows);
   t.nt = __builtin_amdgcn_readfirstlane(t.nt);
-  t.row0 = int64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(t.row0)))) |
-           int64_t(__builtin_amdgcn_readfirstlane(int(t.row0 >> 32))) << 32;
+  t.row0 = uniform(t.row0);
   return t;
 }
 
@@ -308,7 +358,7 @@ struct Side {
   static constexpr int kKRows = 512 / R;            // !KC: values of k in one load
   static constexpr int kRow = R * 2;                // !KC: bytes of an LDS row
 
-  uint32_t voff[kLoads];
+  uint32_t voff;  // this lane's place in load 0; load J goes by a resource that starts `ahead<J>` further
   i32x4 rsrc, rsrc2;  // KC: of the positions whose bit 5 is clear / set (they differ if gated)
   const uint16_t* base;
   int64_t ld;
@@ -327,15 +377,10 @@ struct Side {
     const uint32_t bytes = valid <= 0 ? 0u : uint32_t(valid < R ? valid : R) * uint32_t(ld * 2);
     rsrc = resource(first, bytes);
     rsrc2 = TWO ? resource(second, bytes) : rsrc;
-    const int w = wave_id(), l = lane_id();
-    const int c = (l % 8) ^ (l / 8);
+    const int l = lane_id(), c = (l % 8) ^ (l / 8);
     kc = c * 8;
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-      const int r = (j * W + w) * 8 + l / 8;
-      const int pos = TWO ? (r / 64) * 32 + r % 32 : r;
-      voff[j] = uint32_t(pos) * uint32_t(ld * 2) + c * 16;
-    }
+    const int r = wave_id() * 8 + l / 8;
+    voff = uint32_t(TWO ? r % 32 : r) * uint32_t(ld * 2) + c * 16;
   }
 
   // !KC: `first` points at k 0 of the first position, which is column `col` of its row.
@@ -346,13 +391,21 @@ struct Side {
     tail = __builtin_amdgcn_readfirstlane(int(K_ % kBK));
     skip = __builtin_amdgcn_readfirstlane(col * 2);
     stage_bytes = kBK * uint32_t(ld * 2) - skip;
-    const int w = wave_id(), l = lane_id();
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-      const int k = (j * W + w) * kKRows + l / (R / 8);
-      const int g = ((k & 3) << 1) | (k & 8);
-      voff[j] = uint32_t(k) * uint32_t(ld * 2) + ((l % (R / 8)) ^ g) * 16;
-    }
+    const int l = lane_id(), k = wave_id() * kKRows + l / (R / 8);
+    voff = uint32_t(k) * uint32_t(ld * 2) + ((l % (R / 8)) ^ (((k & 3) << 1) | (k & 8))) * 16;
+  }
+
+  // Rows of the operand between load 0 and load J of a wave.
+  template <int J>
+  static constexpr int kAhead = !KC ? J * W * kKRows : TWO ? J * W * 8 / 64 * 32 : J * W * 8;
+  // The resource of load J: what is behind the rows in front of it.
+  template <int J>
+  __device__ __forceinline__ i32x4 ahead(i32x4 r) const {
+    if constexpr (kAhead<J> == 0) return r;
+    const uint32_t by = kAhead<J> * uint32_t(ld * 2);
+    const uint64_t b = (uint64_t(uint32_t(r[1])) << 32 | uint32_t(r[0])) + by;
+    const int left = r[2] - int(by);
+    return i32x4{int(uint32_t(b)), int(uint32_t(b >> 32)), left > 0 ? left : 0, r[3]};
   }
 
   // The resource that a stage's loads go through: the k of stage `it` (!KC), or the side's own.
@@ -369,12 +422,12 @@ struct Side {
   template <int J, bool WHOLE>
   __device__ __forceinline__ void issue(uint32_t lds, i32x4 r, int it) const {
     if constexpr (!KC) {
-      load_to_lds(lds + J * W * 1024, voff[J], r, 0);
+      load_to_lds(lds + J * W * 1024, voff, ahead<J>(r), 0);
     } else {
-      if (TWO && (W < 8 ? J & 1 : wave_id() >> 2)) r = rsrc2;
+      if (TWO && (W == 8 ? wave_id() >> 2 : J * W >> 2 & 1)) r = rsrc2;
       const bool some = WHOLE || it <= whole;
-      const uint32_t v = WHOLE || it < whole || (it == whole && kc < tail) ? voff[J] : kOutside;
-      load_to_lds(lds + J * W * 1024, v, r, some ? it * (kBK * 2) : 0);
+      const uint32_t v = WHOLE || it < whole || (it == whole && kc < tail) ? voff : kOutside;
+      load_to_lds(lds + J * W * 1024, v, ahead<J>(r), some ? it * (kBK * 2) : 0);
     }
   }
 
@@ -449,113 +502,151 @@ __device__ __forceinline__ int opaque_scalar(int v) {
   return v;
 }
 
-// acc[a][u]: positions 16 u + 4 (lane / 16) .. + 3 of the wave's, against row lane % 16 of its row
-// fragment a, for MREP row fragments.
+// The product of a tile: acc[a][u] is positions 16 u + 4 (lane / 16) .. + 3 of the wave's, against row
+// lane % 16 of its row fragment a, for MREP row fragments.
 //
-// A step takes one stage in two halves of MREP groups of 4 matrix instructions.  While a half is
+// A step takes one stage in two halves of MREP groups of NR matrix instructions.  While a half is
 // computed the next half's fragments are read, each row fragment into the registers that the group
 // before has just used.  The second half reads from the next stage: kHead groups into it stands the
 // barrier that hands that stage over, so that these groups cover the end of the reads and the
 // barrier.  With it the current stage has been read by all, and the loads of the stage ST further on
 // go into its place, spread over the rest of the half: issued together they hold up every wave for
 // as long as the CU's one address unit takes for all of them.
+//
+// The stages of one tile may be followed by those of another: `run` ends with the next tile's first
+// ST stages under way and the first half of its first stage in registers.
 template <typename S, int MREP, typename PS, typename QS>
-__device__ __forceinline__ void product(f32x4 (&acc)[MREP][S::NR], uint8_t* smem, const PS& P,
-                                        const QS& Q, int64_t K) {
-  constexpr int kStage = PS::kBytes + QS::kBytes, ST = S::template kStages<kStage>;
+struct Pipe {
+  static constexpr int kStage = PS::kBytes + QS::kBytes, ST = S::template kStages<kStage>;
   static_assert(ST >= 2, "one stage is computed while the next arrives");
-  constexpr int kLoads = PS::kLoads + QS::kLoads;
-  constexpr int kHead = MREP >= 4 ? 2 : 1, kStep = 16 * S::WM;
-  const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_address(smem));
-  const int w = wave_id(), wm = w % S::WM, wn = w / S::WM;
-#pragma unroll
-  for (int a = 0; a < MREP; ++a)
-#pragma unroll
-    for (int b = 0; b < S::NR; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int n = int((K + kBK - 1) / kBK);
-  if (n == 0) return;
-  uint32_t pb[PS::kBases], qb[QS::kBases], pat[PS::kBases], qat[QS::kBases];
-  PS::template read_bases<16>(pb, lds, wn * S::kWaveN);
-  QS::template read_bases<kStep>(qb, lds + PS::kBytes, wm * 16);
-  auto move_to = [&](int stage) {
-#pragma unroll
-    for (int u = 0; u < (PS::KC ? 2 : 8); ++u) pat[u] = opaque(pb[u] + stage * kStage);
-#pragma unroll
-    for (int u = 0; u < (QS::KC ? 2 : 128 / kStep); ++u) qat[u] = opaque(qb[u] + stage * kStage);
-  };
-  const int dest = opaque_scalar(lds + w * 1024);
-  auto load = [&](auto j, auto whole, int stage, int it, i32x4 pr, i32x4 qr) {
-    if constexpr (j < PS::kLoads)
-      P.template issue<j, whole>(dest + stage * kStage, pr, it);
-    else
-      Q.template issue<j - PS::kLoads, whole>(dest + stage * kStage + PS::kBytes, qr, it);
-  };
-  constexpr std::integral_constant<bool, false> kChecked{};
-#pragma unroll
-  for (int st = 0; st < ST; ++st) {
-    const i32x4 pr = P.template stage_resource<false>(st), qr = Q.template stage_resource<false>(st);
-    static_for<kLoads>([&](auto j) { load(j, kChecked, st, st, pr, qr); });
-  }
+  static constexpr int kLoads = PS::kLoads + QS::kLoads;
+  static constexpr int kHead = MREP >= 4 ? 2 : 1, kStep = 16 * S::WM;
+
+  uint32_t pat[PS::kBases], qat[QS::kBases];  // where this lane reads, in the stage being read
+  int dest, cur;
   bf16x8 p[2][S::NR], q[MREP];
-  // one of the NR + MREP fragments of half `sub`, in the order of use
-  auto read = [&](auto sub, auto i) {
-    if constexpr (i == 0)
-      q[0] = QS::template read<0, kStep, sub>(qat);
-    else if constexpr (i <= S::NR)
-      p[sub][i - 1] = PS::template read<i - 1, 16, sub>(pat);
+
+  __device__ __forceinline__ void move_by(int bytes) {
+#pragma unroll
+    for (int u = 0; u < (PS::KC ? 2 : 8); ++u) pat[u] = opaque(pat[u] + bytes);
+#pragma unroll
+    for (int u = 0; u < (QS::KC ? 2 : 128 / kStep); ++u) qat[u] = opaque(qat[u] + bytes);
+  }
+  template <int J, bool WHOLE>
+  __device__ __forceinline__ void load(const PS& P, const QS& Q, int stage, int it, i32x4 pr,
+                                       i32x4 qr) {
+    if constexpr (J < PS::kLoads)
+      P.template issue<J, WHOLE>(dest + stage * kStage, pr, it);
     else
-      q[i - S::NR] = QS::template read<i - S::NR, kStep, sub>(qat);
-  };
-  // Reads after group a of a half whose first FROM groups read nothing: one row fragment for each
+      Q.template issue<J - PS::kLoads, WHOLE>(dest + stage * kStage + PS::kBytes, qr, it);
+  }
+  // One of the NR + MREP fragments of half SUB, in the order of use.
+  template <int SUB, int I>
+  __device__ __forceinline__ void read() {
+    if constexpr (I == 0)
+      q[0] = QS::template read<0, kStep, SUB>(qat);
+    else if constexpr (I <= S::NR)
+      p[SUB][I - 1] = PS::template read<I - 1, 16, SUB>(pat);
+    else
+      q[I - S::NR] = QS::template read<I - S::NR, kStep, SUB>(qat);
+  }
+  // Reads after group A of a half whose first FROM groups read nothing: one row fragment for each
   // group passed, and P's fragments with the first.
-  auto read_after = [&](auto sub, auto a, auto from) {
-    if constexpr (a == from - 1 || (from == 0 && a == 0)) {
-      static_for<S::NR + 1 + a>([&](auto i) { read(sub, i); });
-    } else if constexpr (a >= from) {
-      read(sub, std::integral_constant<int, a + S::NR>{});
-    }
-  };
-  auto group = [&](auto sub, auto a) {
+  template <int SUB, int A, int FROM>
+  __device__ __forceinline__ void read_after() {
+    if constexpr (A == FROM - 1 || (FROM == 0 && A == 0))
+      static_for<S::NR + 1 + A>([&](auto i) { read<SUB, i>(); });
+    else if constexpr (A >= FROM)
+      read<SUB, A + S::NR>();
+  }
+  template <int SUB, int A>
+  __device__ __forceinline__ void group(f32x4 (&acc)[MREP][S::NR]) {
 #pragma unroll
     for (int u = 0; u < S::NR; ++u)
-      acc[a][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p[sub][u], q[a], acc[a][u], 0, 0, 0);
+      acc[A][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p[SUB][u], q[A], acc[A][u], 0, 0, 0);
     __builtin_amdgcn_sched_barrier(0);
-  };
-  constexpr std::integral_constant<int, 0> kFirst{};
-  constexpr std::integral_constant<int, 1> kSecond{};
-  stage_ready<(ST - 1) * kLoads>();
-  move_to(0);
-  static_for<S::NR + MREP>([&](auto i) { read(kFirst, i); });
-  int cur = 0, it = 0;
-  auto step = [&](auto whole) {
+  }
+
+  // Start the first tile's first ST stages.
+  __device__ __forceinline__ void begin(uint8_t* smem, const PS& P, const QS& Q) {
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_address(smem));
+    const int w = wave_id(), wm = w % S::WM, wn = w / S::WM;
+    PS::template read_bases<16>(pat, lds, wn * S::kWaveN);
+    QS::template read_bases<kStep>(qat, lds + PS::kBytes, wm * 16);
+    dest = opaque_scalar(lds + w * 1024);
+    cur = 0;
+#pragma unroll
+    for (int st = 0; st < ST; ++st) {
+      const i32x4 pr = P.template stage_resource<false>(st), qr = Q.template stage_resource<false>(st);
+      static_for<kLoads>([&](auto j) { load<j, false>(P, Q, st, st, pr, qr); });
+    }
+  }
+  // Wait for the first of them and read its first half.
+  __device__ __forceinline__ void first_half() {
+    stage_ready<(ST - 1) * kLoads>();
+    move_by(0);
+    static_for<S::NR + MREP>([&](auto i) { read<0, i>(); });
+  }
+
+  // P, Q: the sides the loads of stage `it` go by.
+  template <bool WHOLE>
+  __device__ __forceinline__ void step(f32x4 (&acc)[MREP][S::NR], const PS& P, const QS& Q, int it) {
     static_for<MREP>([&](auto a) {
-      group(kFirst, a);
-      read_after(kSecond, a, std::integral_constant<int, 0>{});
+      group<0, a>(acc);
+      read_after<1, a, 0>();
       __builtin_amdgcn_sched_barrier(0);
     });
     const int nxt = cur == ST - 1 ? 0 : cur + 1;
     i32x4 pr, qr;
     static_for<MREP>([&](auto a) {
-      group(kSecond, a);
+      group<1, a>(acc);
       if constexpr (a == kHead - 1) {
-        move_to(nxt);
-        pr = P.template stage_resource<whole>(it + ST);
-        qr = Q.template stage_resource<whole>(it + ST);
+        move_by((nxt - cur) * kStage);
+        pr = P.template stage_resource<WHOLE>(it);
+        qr = Q.template stage_resource<WHOLE>(it);
         stage_ready<(ST - 2) * kLoads>();
       }
-      read_after(kFirst, a, std::integral_constant<int, kHead>{});
+      read_after<0, a, kHead>();
       static_for<kLoads>([&](auto j) {
         constexpr int at = kHead - 1 + j * (MREP - kHead + 1) / kLoads;
-        if constexpr (a == at) load(j, whole, cur, it + ST, pr, qr);
+        if constexpr (a == at) load<j, WHOLE>(P, Q, cur, it, pr, qr);
       });
       __builtin_amdgcn_sched_barrier(0);
     });
     cur = nxt;
-    ++it;
-  };
-  const int fast = min(P.whole, Q.whole) - ST;
-  while (it < fast) step(std::integral_constant<bool, true>{});
-  while (it < n) step(kChecked);
+  }
+
+  // acc = the product over P's and Q's n >= ST stages; the stages that follow are those of PN and QN.
+  __device__ __forceinline__ void run(f32x4 (&acc)[MREP][S::NR], const PS& P, const QS& Q, int n,
+                                      const PS& PN, const QS& QN) {
+#pragma unroll
+    for (int a = 0; a < MREP; ++a)
+#pragma unroll
+      for (int b = 0; b < S::NR; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int fast = min(P.whole, Q.whole);
+    int it = ST;
+    for (; it < fast; ++it) step<true>(acc, P, Q, it);
+    for (; it < n; ++it) step<false>(acc, P, Q, it);
+    for (; it < n + ST; ++it) step<false>(acc, PN, QN, it - n);
+  }
+};
+
+// One tile alone.
+template <typename S, int MREP, typename PS, typename QS>
+__device__ __forceinline__ void product(f32x4 (&acc)[MREP][S::NR], uint8_t* smem, const PS& P,
+                                        const QS& Q, int64_t K) {
+  Pipe<S, MREP, PS, QS> pipe;
+  pipe.begin(smem, P, Q);
+  pipe.first_half();
+#pragma unroll
+  for (int a = 0; a < MREP; ++a)
+#pragma unroll
+    for (int b = 0; b < S::NR; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  constexpr int ST = Pipe<S, MREP, PS, QS>::ST;
+  const int n = int((K + kBK - 1) / kBK), fast = min(P.whole, Q.whole);
+  int it = ST;
+  for (; it < fast; ++it) pipe.template step<true>(acc, P, Q, it);
+  for (; it < n + ST; ++it) pipe.template step<false>(acc, P, Q, it);
   // Loads still under way write zeros to LDS, and other waves may still read it: both end before it
   // is used again.
   stage_ready<0>();
@@ -584,15 +675,15 @@ __device__ __forceinline__ f32x4 act4(f32x4 v, int act) {
 // v[1]; GATED: n is the column among the tile's gate columns, v[2], v[3] the same columns' up.  Rows
 // from `rows` on are left out.
 //
-// The sums go through LDS, which the product no longer needs, 4 row fragments of a wave at a time,
+// The sums go through LDS, FRAGS (or up to 4) row fragments of a wave at a time,
 // each wave through a part of its own: what follows is then one loop over rows, whole rows of a wave
 // (256 bytes of bf16) leave together, and an activation's code is there once and not for each of 256
 // registers.  It costs 2 us of a 256 x 256 tile's 60 to 200 us.  Chunk c (16 bytes) of row r sits in
 // slot c ^ (r & 15), so that the 16 rows that one write serves differ in their banks.
-template <typename S, bool GATED, int MREP, typename F>
+template <typename S, bool GATED, int FRAGS = 0, int MREP, typename F>
 __device__ __forceinline__ void each_row(const f32x4 (&acc)[MREP][S::NR], uint8_t* smem, int rows,
                                          F f) {
-  constexpr int kFrags = MREP <= 4 ? MREP : MREP % 3 == 0 ? 3 : 4;
+  constexpr int kFrags = FRAGS ? FRAGS : MREP <= 4 ? MREP : MREP % 3 == 0 ? 3 : 4;
   static_assert(MREP % kFrags == 0, "");
   constexpr int kRowBytes = S::kWaveN * 4, kPart = kFrags * 16 * kRowBytes;
   constexpr int kLanes = S::kWaveN / (GATED ? 16 : 8);  // lanes of one row
@@ -659,13 +750,13 @@ __device__ __forceinline__ void by_height(int rows, F f) {
 // h = act(x Wg^T) * (x Wu^T): each wave's 64 positions are 32 gate columns and the same 32 up
 // columns, so that one lane has both factors.
 template <typename S>
-__global__ __launch_bounds__(S::kThreads) void gated_kernel(
+__global__ __launch_bounds__(S::kThreads, 2) void gated_kernel(
     const uint16_t* x, const int32_t* off, const uint16_t* w, int64_t rows, int E, int H, int I,
     int act, uint16_t* h, uint16_t* gu) {
   __shared__ __align__(1024) uint8_t smem[S::kLds];
   constexpr int kCols = S::BN / 2;
   const int ncol = (I + kCols - 1) / kCols;
-  for (int64_t id = blockIdx.x;; id += gridDim.x) {
+  for (uint32_t id = blockIdx.x;; id += gridDim.x) {
     const Tile t = find_tile<S::FULL, S::BM, S::kThreads>(off, E, rows, ncol, id);
     if (t.e < 0) return;
     const int n0 = t.nt * kCols;
@@ -695,12 +786,12 @@ __global__ __launch_bounds__(S::kThreads) void gated_kernel(
 
 // y = act(x W^T + bias) + residual, pre = act's argument.
 template <typename S>
-__global__ __launch_bounds__(S::kThreads) void matmul_kernel(
+__global__ __launch_bounds__(S::kThreads, 2) void matmul_kernel(
     const uint16_t* x, const int32_t* off, const uint16_t* w, const uint16_t* bias,
     const uint16_t* res, int64_t rows, int E, int K, int N, int act, uint16_t* y, uint16_t* pre) {
   __shared__ __align__(1024) uint8_t smem[S::kLds];
   const int ncol = (N + S::BN - 1) / S::BN;
-  for (int64_t id = blockIdx.x;; id += gridDim.x) {
+  for (uint32_t id = blockIdx.x;; id += gridDim.x) {
     const Tile t = find_tile<S::FULL, S::BM, S::kThreads>(off, E, rows, ncol, id);
     if (t.e < 0) return;
     const int n0 = t.nt * S::BN;
@@ -740,12 +831,12 @@ __global__ __launch_bounds__(S::kThreads) void matmul_kernel(
 
 // dx = d W: the weights [N, K] are contiguous along the output's own index.
 template <typename S>
-__global__ __launch_bounds__(S::kThreads) void data_grad_kernel(
+__global__ __launch_bounds__(S::kThreads, 2) void data_grad_kernel(
     const uint16_t* d, const int32_t* off, const uint16_t* w, int64_t rows, int E, int N, int K,
     uint16_t* dx) {
   __shared__ __align__(1024) uint8_t smem[S::kLds];
   const int ncol = (K + S::BN - 1) / S::BN;
-  for (int64_t id = blockIdx.x;; id += gridDim.x) {
+  for (uint32_t id = blockIdx.x;; id += gridDim.x) {
     const Tile t = find_tile<S::FULL, S::BM, S::kThreads>(off, E, rows, ncol, id);
     if (t.e < 0) return;
     const int n0 = t.nt * S::BN;
@@ -768,29 +859,112 @@ __global__ __launch_bounds__(S::kThreads) void data_grad_kernel(
 
 // dW[e] = d^T x over the expert's rows: both sides are contiguous along the
 // output's indexes.  An expert without rows gets zeros.
+//
+// With some hundred rows an expert a tile is over after a few stages, and its start (2 us until the
+// first loads arrive) and its end (5 us of stores) cost as much as its product.  So one block a CU
+// goes through its tiles as one sequence of stages: the next tile's first stages arrive while the
+// current one's last are computed, and the sums leave through LDS of their own while they do.  A
+// tile is at least ST stages long for that, the added ones all zeros.
 template <typename S, bool F32>
-__global__ __launch_bounds__(S::kThreads) void weight_grad_kernel(
+__global__ __launch_bounds__(S::kThreads, 2) void weight_grad_kernel(
+    const uint16_t* d, const uint16_t* x, const int32_t* off, int64_t rows, int E, int N, int K,
+    void* dw) {
+  typedef Side<false, S::BN, S::W> PS;
+  typedef Side<false, S::BM, S::W> QS;
+  typedef Pipe<S, S::MR, PS, QS> Pipeline;
+  __shared__ __align__(1024) uint8_t smem[Pipeline::ST * Pipeline::kStage];
+  __shared__ __align__(1024) uint8_t sums[S::W * 16 * S::kWaveN * 4];
+  const uint32_t nn = (N + S::BM - 1) / S::BM, nk = (K + S::BN - 1) / S::BN;
+  const uint32_t total = E * nn * nk;
+  struct Place {
+    uint32_t id;
+    int e, m0, n0, n;  // n stages; 0 behind the last tile
+  };
+  auto put = [&](const Place& t, int m, int c, const f32x4(&v)[2]) {
+    if (t.n0 + c >= K) return;
+    const int64_t at = (int64_t(t.e) * N + t.m0 + m) * K + t.n0 + c;
+    if (F32) {
+      f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(dw) + at);
+      o[0] = v[0];
+      o[1] = v[1];
+    } else {
+      store8(static_cast<uint16_t*>(dw) + at, v[0], v[1]);
+    }
+  };
+  // The first tile from number `id` on that has rows, and its sides; tiles without are written on the
+  // way.
+  auto find = [&](uint32_t id, Place& t, PS& P, QS& Q) {
+    t = Place{};
+    int64_t lo = 0, cnt = 0;
+    for (; id < total; id += gridDim.x) {
+      const uint32_t seq = xcd_order(id, total);
+      t.e = int(seq / (nn * nk));
+      int mt, ct;
+      grid_order(seq - uint32_t(t.e) * nn * nk, nn, nk, mt, ct);
+      t.m0 = mt * S::BM;
+      t.n0 = ct * S::BN;
+      expert_rows_scalar(off, t.e, rows, lo, cnt);
+      if (cnt > 0) break;
+      const f32x4 zero[2] = {};
+      for (int i = threadIdx.x; i < S::BM * (S::BN / 8); i += S::kThreads) {
+        const int m = i / (S::BN / 8);
+        if (t.m0 + m < N) put(t, m, i % (S::BN / 8) * 8, zero);
+      }
+    }
+    t.id = id;
+    if (cnt > 0) {
+      const int n = int((cnt + kBK - 1) / kBK);
+      t.n = n < Pipeline::ST ? Pipeline::ST : n;
+    }
+    P.init_mc(x + lo * K + t.n0, K, cnt, t.n0);
+    Q.init_mc(d + lo * N + t.m0, N, cnt, t.m0);
+  };
+  Place t, next;
+  PS P, PN;
+  QS Q, QN;
+  find(blockIdx.x, t, P, Q);
+  if (t.n == 0) return;
+  Pipeline pipe;
+  pipe.begin(smem, P, Q);
+  pipe.first_half();
+  f32x4 acc[S::MR][S::NR];
+  do {
+    find(t.id + gridDim.x, next, PN, QN);
+    pipe.run(acc, P, Q, t.n, PN, QN);
+    each_row<S, false, 1>(acc, sums, N - t.m0, [&](int m, int c, const f32x4(&v)[2]) {
+      put(t, m, c, v);
+    });
+    t = next;
+    P = PN;
+    Q = QN;
+  } while (t.n > 0);
+  stage_ready<0>();  // the loads behind the last tile
+}
+
+// The same, a block a tile.
+template <typename S, bool F32>
+__global__ __launch_bounds__(S::kThreads, 2) void weight_grad_alone_kernel(
     const uint16_t* d, const uint16_t* x, const int32_t* off, int64_t rows, int E, int N, int K,
     void* dw) {
   __shared__ __align__(1024) uint8_t smem[S::kLds];
-  const int64_t nn = (N + S::BM - 1) / S::BM, nk = (K + S::BN - 1) / S::BN;
-  const int64_t total = E * nn * nk;
-  for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
-    const int64_t seq = xcd_order(id, total);
+  const uint32_t nn = (N + S::BM - 1) / S::BM, nk = (K + S::BN - 1) / S::BN;
+  const uint32_t total = E * nn * nk;
+  for (uint32_t id = blockIdx.x; id < total; id += gridDim.x) {
+    const uint32_t seq = xcd_order(id, total);
     const int e = int(seq / (nn * nk));
-    int64_t mt, ct;
-    grid_order(seq - e * nn * nk, nn, nk, mt, ct);
-    const int m0 = int(mt) * S::BM, n0 = int(ct) * S::BN;
+    int mt, ct;
+    grid_order(seq - uint32_t(e) * nn * nk, nn, nk, mt, ct);
+    const int m0 = mt * S::BM, n0 = ct * S::BN;
     int64_t lo, cnt;
-    expert_rows(off, e, rows, lo, cnt);
-    const uint16_t* xe = x + lo * K + n0;
-    const uint16_t* de = d + lo * N + m0;
-    Side<false, S::BN, S::W> P;
-    Side<false, S::BM, S::W> Q;
-    P.init_mc(xe, K, cnt, n0);
-    Q.init_mc(de, N, cnt, m0);
-    f32x4 acc[S::MR][S::NR];
-    product<S, S::MR>(acc, smem, P, Q, cnt);
+    expert_rows_scalar(off, e, rows, lo, cnt);
+    f32x4 acc[S::MR][S::NR] = {};
+    if (cnt > 0) {
+      Side<false, S::BN, S::W> P;
+      Side<false, S::BM, S::W> Q;
+      P.init_mc(x + lo * K + n0, K, cnt, n0);
+      Q.init_mc(d + lo * N + m0, N, cnt, m0);
+      product<S, S::MR>(acc, smem, P, Q, cnt);
+    }
     each_row<S, false>(acc, smem, N - m0, [&](int m, int c, const f32x4(&v)[2]) {
       if (n0 + c >= K) return;
       const int64_t at = (int64_t(e) * N + m0 + m) * K + n0 + c;
@@ -946,13 +1120,23 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 bool bad_features(int32_t n) { return n < 8 || n > kMaxFeatures; }
 
-// The sizes every product shares; MOE_OK with rows == 0 allowed.
+// One block of 8 waves a CU: two stages of 32 KiB of weights and up to 40 KiB of rows.
+using Tall = Shape<256, 288, 256, 2, 4, 144 * 1024>;
+using Square = Shape<256, 256, 256, 2, 4, 128 * 1024>;
+using Half = Shape<128, 128, 128, 2, 2, 72 * 1024>;  // 4 waves, two blocks a CU
+
+// The sizes every product shares; MOE_OK with rows == 0 allowed.  Tile numbers are 32-bit: what a
+// call could need at most has to stay below 2^31, far beyond any buffers that fit the card.
 int check_sizes(int64_t rows, int32_t E, int32_t a, int32_t b, int32_t act, bool none_ok) {
   if (rows < 0 || rows > kMaxPairs || E < 1 || E > kMaxE) return MOE_ERR_INVALID_ARG;
   if (bad_features(a) || bad_features(b)) return MOE_ERR_INVALID_ARG;
   if (act < (none_ok ? MOE_ACT_NONE : MOE_ACT_SILU) || act > MOE_ACT_RELU)
     return MOE_ERR_INVALID_ARG;
   if (a % 8 != 0 || b % 8 != 0) return MOE_ERR_ALIGNMENT;
+  const int64_t ca = a / 64 + 1, cb = b / 64 + 1;  // columns of the narrowest tiles
+  const int64_t tall = rows / Half::FULL + E;
+  if (tall * ca > kMaxTiles || tall * cb > kMaxTiles || ca * cb > kMaxTiles / E)
+    return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 
@@ -962,13 +1146,15 @@ int64_t row_tile_blocks(int64_t rows, int32_t E, int bm, int64_t cols) {
   return (rows / bm + (rows < E ? rows : E)) * cols;
 }
 
-// Whether the experts have too few rows each for the tall tiles.
-bool few_rows(int64_t rows, int32_t E) { return rows <= int64_t(E) * 32; }
-
-// One block of 8 waves a CU: two stages of 32 KiB of weights and up to 40 KiB of rows.
-using Tall = Shape<256, 288, 256, 2, 4, 144 * 1024>;
-using Square = Shape<256, 256, 256, 2, 4, 128 * 1024>;
-using Small = Shape<64, 64, 128, 2, 2, 96 * 1024>;  // 4 waves
+// Whether a product over the experts' rows takes Half tiles: under 128 rows an expert (the tall
+// tiles' heights are then mostly empty, and two blocks a CU cover each other's waits), or so few tall
+// tiles that half of the CUs would have none.  `cols`: outputs to a tall tile's row.
+// Measured, rows spread at random, tall against half tiles: 64 experts of 2048 x 2048, 64 rows each,
+// 142 against 127 us, 128 rows 153 against 158, 256 rows 183 against 212; 16 of 4096 x 4096, 64 rows
+// 134 against 116, 128 rows 146 against 179; 8 of 520 x 1280, 512 rows 30 against 19.
+bool half_tiles(int64_t rows, int32_t E, int64_t cols) {
+  return rows < int64_t(E) * 128 || row_tile_blocks(rows, E, Tall::FULL, cols) <= kCus / 2;
+}
 
 }  // namespace
 
@@ -991,7 +1177,9 @@ int moe_expert_gated(const void* x, const int32_t* expert_offsets, const void* w
                   static_cast<const uint16_t*>(w_gate_up), rows, E, H, I, act,
                   static_cast<uint16_t*>(h), static_cast<uint16_t*>(gate_up));
   };
-  return few_rows(rows, E) ? run(Small{}, gated_kernel<Small>) : run(Tall{}, gated_kernel<Tall>);
+  return half_tiles(rows, E, (I + Tall::BN / 2 - 1) / (Tall::BN / 2))
+             ? run(Half{}, gated_kernel<Half>)
+             : run(Tall{}, gated_kernel<Tall>);
 }
 
 int moe_expert_matmul(const void* x, const int32_t* expert_offsets, const void* w,
@@ -1011,24 +1199,43 @@ int moe_expert_matmul(const void* x, const int32_t* expert_offsets, const void* 
                   static_cast<const uint16_t*>(bias), static_cast<const uint16_t*>(residual), rows,
                   E, K, N, act, static_cast<uint16_t*>(y), static_cast<uint16_t*>(pre));
   };
-  return few_rows(rows, E) ? run(Small{}, matmul_kernel<Small>) : run(Tall{}, matmul_kernel<Tall>);
+  return half_tiles(rows, E, (N + Tall::BN - 1) / Tall::BN)
+             ? run(Half{}, matmul_kernel<Half>)
+             : run(Tall{}, matmul_kernel<Tall>);
 }
 
 static int weight_grad(const void* d, const void* x, const int32_t* off, int64_t rows, int E,
                        int N, int K, void* dw, int dw_f32, hipStream_t s) {
-  const int64_t n = int64_t(E) * ((N + Square::BM - 1) / Square::BM) * ((K + Square::BN - 1) / Square::BN);
-  return launch(dw_f32 ? weight_grad_kernel<Square, true> : weight_grad_kernel<Square, false>,
-                n, Square::kThreads, s,
-                static_cast<const uint16_t*>(d), static_cast<const uint16_t*>(x), off, rows, E, N,
-                K, dw);
+  auto run = [&](auto shape, auto kern, int64_t most) {
+    using S = decltype(shape);
+    const int64_t n = int64_t(E) * ((N + S::BM - 1) / S::BM) * ((K + S::BN - 1) / S::BN);
+    return launch(kern, n < most ? n : most, S::kThreads, s, static_cast<const uint16_t*>(d),
+                  static_cast<const uint16_t*>(x), off, rows, E, N, K, dw);
+  };
+  // So few square tiles that they fill the CUs once at best go in halves, a block each: 16 experts of
+  // 1288 x 520 (288 square tiles) take 12.0 us in halves, 15.8 as square ones with a block each; 64 of
+  // 2048 x 2048 take 123 us in one sequence of square tiles a CU, 152 with a block each, 173 in halves
+  // (16 rows an expert), and 235, 260 and 310 us (256 rows).
+  const int64_t square = int64_t(E) * ((N + Square::BM - 1) / Square::BM) *
+                         ((K + Square::BN - 1) / Square::BN);
+  if (square <= kCus + kCus / 4)
+    return dw_f32 ? run(Half{}, weight_grad_alone_kernel<Half, true>, kMaxBlocks)
+                  : run(Half{}, weight_grad_alone_kernel<Half, false>, kMaxBlocks);
+  return dw_f32 ? run(Square{}, weight_grad_kernel<Square, true>, kCus)
+                : run(Square{}, weight_grad_kernel<Square, false>, kCus);
 }
 
 static int data_grad(const void* d, const int32_t* off, const void* w, int64_t rows, int E, int N,
                      int K, void* dx, hipStream_t s) {
-  return launch(data_grad_kernel<Tall>,
-                row_tile_blocks(rows, E, Tall::FULL, (K + Tall::BN - 1) / Tall::BN), Tall::kThreads, s,
-                static_cast<const uint16_t*>(d), off, static_cast<const uint16_t*>(w), rows, E, N,
-                K, static_cast<uint16_t*>(dx));
+  auto run = [&](auto shape, auto kern) {
+    using S = decltype(shape);
+    return launch(kern, row_tile_blocks(rows, E, S::FULL, (K + S::BN - 1) / S::BN), S::kThreads, s,
+                  static_cast<const uint16_t*>(d), off, static_cast<const uint16_t*>(w), rows, E, N,
+                  K, static_cast<uint16_t*>(dx));
+  };
+  return half_tiles(rows, E, (K + Tall::BN - 1) / Tall::BN)
+             ? run(Half{}, data_grad_kernel<Half>)
+             : run(Tall{}, data_grad_kernel<Tall>);
 }
 
 int moe_expert_gated_backward(const void* dh, const void* gate_up, const void* x,

@@ -19,13 +19,12 @@ and back
 """
 from __future__ import annotations
 
-import contextlib
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import _lib
-from .binding import _check, _dev, _empty, _stream
+from .binding import MoeError, _dev, _empty, _stream
 
 _BF16 = torch.bfloat16
 
@@ -50,12 +49,22 @@ def _act(act: str) -> int:
         raise ValueError(f"act must be one of {sorted(_lib.ACTS)}, got {act!r}") from None
 
 
-def _at(device: int):
-    """Context that makes `device` the current one: a launch goes to the
-    current device, so tensors elsewhere need the switch."""
-    if device == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+# The current device without the checks of torch.cuda.current_device, which
+# cost as much as the rest of a small call's marshalling.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _call(name: str, device: int, *args) -> None:
+    """The library's entry point `name`, with `device` the current one: a
+    launch goes to the current device, so tensors elsewhere need the switch."""
+    fn = getattr(_lib.load(), name)
+    if device == _current_device():
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    if status != _lib.MOE_OK:
+        raise MoeError(name, status)
 
 
 def _given(t: Optional[torch.Tensor], name: str, shape, dtype, device: int) -> Optional[int]:
@@ -63,7 +72,7 @@ def _given(t: Optional[torch.Tensor], name: str, shape, dtype, device: int) -> O
     if t is None:
         return None
     p = _dev(t, name, dtype, len(shape), device)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     return p
 
@@ -71,7 +80,9 @@ def _given(t: Optional[torch.Tensor], name: str, shape, dtype, device: int) -> O
 def _out(t: Optional[torch.Tensor], name: str, shape, dtype, like: torch.Tensor, stream):
     """(tensor, pointer) of an output, allocated on the launch stream if not given."""
     if t is None:
-        t = _empty(shape, dtype, like, stream)
+        t = like.new_empty(shape, dtype=dtype) if stream is None else _empty(shape, dtype, like,
+                                                                            stream)
+        return t, t.data_ptr()
     return t, _given(t, name, shape, dtype, like.get_device())
 
 
@@ -107,9 +118,7 @@ def moe_expert_gated(x: torch.Tensor, expert_offsets: torch.Tensor, w_gate_up: t
     gp = None
     if save_gate_up or gate_up is not None:
         gate_up, gp = _out(gate_up, "gate_up", (rows, I2), _BF16, x, stream)
-    with _at(d):
-        _check("moe_expert_gated", _lib.load().moe_expert_gated(
-            xp, op, wp, rows, E, H, I2 // 2, a, hp, gp, _stream(stream, x)))
+    _call("moe_expert_gated", d, xp, op, wp, rows, E, H, I2 // 2, a, hp, gp, _stream(stream, x))
     return h, gate_up
 
 
@@ -140,10 +149,8 @@ def moe_expert_gated_backward(dh: torch.Tensor, gate_up: torch.Tensor, x: torch.
         dx, dxp = _out(dx, "dx", (rows, H), _BF16, x, stream)
     if need_dw or dw is not None:
         dw, dwp = _out(dw, "dw", (E, I2, H), wt, x, stream)
-    with _at(d):
-        _check("moe_expert_gated_backward", _lib.load().moe_expert_gated_backward(
-            hp, gp, xp, op, wp, rows, E, H, I2 // 2, a, dgp, dxp, dwp, int(wt is torch.float32),
-            _stream(stream, x)))
+    _call("moe_expert_gated_backward", d, hp, gp, xp, op, wp, rows, E, H, I2 // 2, a, dgp, dxp,
+          dwp, int(wt is torch.float32), _stream(stream, x))
     return GatedGrads(dx, dw, dgate_up)
 
 
@@ -170,9 +177,7 @@ def moe_expert_matmul(x: torch.Tensor, expert_offsets: torch.Tensor, w: torch.Te
     pp = None
     if save_pre or pre is not None:
         pre, pp = _out(pre, "pre", (rows, N), _BF16, x, stream)
-    with _at(d):
-        _check("moe_expert_matmul", _lib.load().moe_expert_matmul(
-            xp, op, wp, bp, rp, rows, E, K, N, a, yp, pp, _stream(stream, x)))
+    _call("moe_expert_matmul", d, xp, op, wp, bp, rp, rows, E, K, N, a, yp, pp, _stream(stream, x))
     return y, pre
 
 
@@ -212,10 +217,8 @@ def moe_expert_matmul_backward(dy: torch.Tensor, x: torch.Tensor, expert_offsets
         dw, dwp = _out(dw, "dw", (E, N, K), wt, x, stream)
     if need_dbias or dbias is not None:
         dbias, dbp = _out(dbias, "dbias", (E, N), torch.float32, x, stream)
-    with _at(d):
-        _check("moe_expert_matmul_backward", _lib.load().moe_expert_matmul_backward(
-            yp, pp, xp, op, wp, rows, E, K, N, a, dpp, dxp, dwp, int(wt is torch.float32), dbp,
-            _stream(stream, x)))
+    _call("moe_expert_matmul_backward", d, yp, pp, xp, op, wp, rows, E, K, N, a, dpp, dxp, dwp,
+          int(wt is torch.float32), dbp, _stream(stream, x))
     return MatmulGrads(dx, dw, dbias, dpre)
 
 
@@ -240,7 +243,5 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, pair_row: torch.Te
         raise ValueError("capacity exceeds y's rows")
     dy, dyp = _out(dy, "dy", (y.shape[0], H), _BF16, y, stream)
     dtopk_w, dwp = _out(dtopk_w, "dtopk_w", (T, k), torch.float32, y, stream)
-    with _at(d):
-        _check("moe_combine_backward", _lib.load().moe_combine_backward(
-            op, yp, pp, wp, T, H, k, capacity, dyp, dwp, _stream(stream, y)))
+    _call("moe_combine_backward", d, op, yp, pp, wp, T, H, k, capacity, dyp, dwp, _stream(stream, y))
     return dy, dtopk_w

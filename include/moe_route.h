@@ -370,7 +370,9 @@ int moe_combine(const void* y, const int32_t* pair_row, const float* topk_w,
  *    no rows.  Rows outside every expert (behind expert_offsets[E]) are left
  *    as they were in every output.
  *  - Features (H, I, K, N) are multiples of 8 between 8 and 2^20; every bf16
- *    pointer is 16-byte aligned.  1 <= E <= 1024.
+ *    pointer is 16-byte aligned.  1 <= E <= 1024.  Sizes whose tiles (128 rows
+ *    or features by 64) would number 2^31 or more are MOE_ERR_INVALID_ARG; no
+ *    buffers of such sizes fit the card.
  *  - Rows and weights are bf16; products accumulate in fp32 and each output is
  *    rounded once, from fp32.  The order of a sum does not depend on the
  *    timing of the run: repeated calls give the same bits.
