@@ -337,6 +337,16 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t voff, i32x4 r
       : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff));
 }
 
+// The same for data that no other block reads: it is not kept in the caches.
+__device__ __forceinline__ void load_once_to_lds(uint32_t lds, uint32_t voff, i32x4 rsrc, int soff) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, %3 offen nt lds"
+      :
+      : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff));
+}
+
 // All but the newest N loads of this wave have arrived and its LDS reads are
 // done; then the same holds for every wave of the block.
 template <int N>
@@ -350,7 +360,7 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 }
 
 // One side of R positions, loaded by W waves.
-template <bool KC_, int R, int W, bool TWO = false>
+template <bool KC_, int R, int W, bool TWO = false, bool ONCE = false>
 struct Side {
   static constexpr bool KC = KC_;
   static constexpr int kBytes = R * kBK * 2;
@@ -417,28 +427,37 @@ struct Side {
     return resource(base + (WHOLE || it <= whole ? int64_t(it) * kBK * ld : 0), n);
   }
 
+  static __device__ __forceinline__ void bring(uint32_t lds, uint32_t v, i32x4 r, int soff) {
+    if constexpr (ONCE)
+      load_once_to_lds(lds, v, r, soff);
+    else
+      load_to_lds(lds, v, r, soff);
+  }
+
   // Start this wave's load J of the stage at `lds` (this wave's first KiB of the side there), which
   // takes k in [64 it, 64 it + 64).  WHOLE: all of these exist.
   template <int J, bool WHOLE>
   __device__ __forceinline__ void issue(uint32_t lds, i32x4 r, int it) const {
     if constexpr (!KC) {
-      load_to_lds(lds + J * W * 1024, voff, ahead<J>(r), 0);
+      bring(lds + J * W * 1024, voff, ahead<J>(r), 0);
     } else {
       if (TWO && (W == 8 ? wave_id() >> 2 : J * W >> 2 & 1)) r = rsrc2;
       const bool some = WHOLE || it <= whole;
       const uint32_t v = WHOLE || it < whole || (it == whole && kc < tail) ? voff : kOutside;
-      load_to_lds(lds + J * W * 1024, v, ahead<J>(r), some ? it * (kBK * 2) : 0);
+      bring(lds + J * W * 1024, v, ahead<J>(r), some ? it * (kBK * 2) : 0);
     }
   }
 
-  // Where this lane reads in the side's part of a stage, by half stage (KC) or fragment: the address
-  // of fragment 0, or of the first 128 / STEP fragments (256 bytes on, the swizzle is the same).  Fragment f is positions row0 + f * STEP .. + 15.
-  static constexpr int kBases = KC ? 2 : 8;
-  template <int STEP>
-  static __device__ __forceinline__ void read_bases(uint32_t (&at)[kBases], uint32_t lds, int row0) {
+  // Where this lane reads in the side's part of a stage: KC, the address of fragment 0 in each half
+  // stage; else that of each of the first 128 / STEP fragments (256 bytes on, the swizzle is the same).
+  // Fragment f is positions row0 + f * STEP .. + 15, f < FRAGS.
+  template <int STEP, int FRAGS>
+  static constexpr int kBases = KC ? 2 : FRAGS < 128 / STEP ? FRAGS : 128 / STEP;
+  template <int STEP, int N>
+  static __device__ __forceinline__ void read_bases(uint32_t (&at)[N], uint32_t lds, int row0) {
     const int l = lane_id(), i = l % 16, q = l / 16;
 #pragma unroll
-    for (int u = 0; u < (KC ? 2 : 128 / STEP); ++u) {
+    for (int u = 0; u < N; ++u) {
       if (KC) {
         at[u] = lds + (row0 + i) * 128 + (((u * 4 + q) ^ (i & 7)) * 16);
       } else {
@@ -450,8 +469,8 @@ struct Side {
   }
 
   // Fragment F of half stage SUB, 8 values of k per lane, of the stage `at` was moved to.
-  template <int F, int STEP, int SUB>
-  static __device__ __forceinline__ bf16x8 read(const uint32_t (&at)[kBases]) {
+  template <int F, int STEP, int SUB, int N>
+  static __device__ __forceinline__ bf16x8 read(const uint32_t (&at)[N]) {
     typedef __attribute__((address_space(3))) const bf16x8* Frag;
     typedef __attribute__((address_space(3))) s16x4* Tr;
     if constexpr (KC) {
@@ -477,8 +496,9 @@ __device__ __forceinline__ void static_for(F f) {
 
 // The tile shape: up to BM x BN outputs (rows are cut by FULL, see cut_rows) by WM x WN waves.  A wave's
 // row fragment i covers rows 16 (i * WM + wave row), so that a short tile loads every wave alike.
-template <int FULL_, int BM_, int BN_, int WM_, int WN_, int LDS_>
+template <int FULL_, int BM_, int BN_, int WM_, int WN_, int LDS_, bool ONCE = false>
 struct Shape {
+  static constexpr bool kOnce = ONCE;  // the weights are read by one block each
   static constexpr int FULL = FULL_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, kLds = LDS_;
   static constexpr int W = WM * WN, kThreads = W * kWave;
   static constexpr int kWaveN = BN / WN, MR = BM / WM / 16, NR = kWaveN / 16;
@@ -522,15 +542,17 @@ struct Pipe {
   static constexpr int kLoads = PS::kLoads + QS::kLoads;
   static constexpr int kHead = MREP >= 4 ? 2 : 1, kStep = 16 * S::WM;
 
-  uint32_t pat[PS::kBases], qat[QS::kBases];  // where this lane reads, in the stage being read
+  static constexpr int kPB = PS::template kBases<16, S::NR>, kQB = QS::template kBases<kStep, MREP>;
+
+  uint32_t pat[kPB], qat[kQB];  // where this lane reads, in the stage being read
   int dest, cur;
   bf16x8 p[2][S::NR], q[MREP];
 
   __device__ __forceinline__ void move_by(int bytes) {
 #pragma unroll
-    for (int u = 0; u < (PS::KC ? 2 : 8); ++u) pat[u] = opaque(pat[u] + bytes);
+    for (int u = 0; u < kPB; ++u) pat[u] = opaque(pat[u] + bytes);
 #pragma unroll
-    for (int u = 0; u < (QS::KC ? 2 : 128 / kStep); ++u) qat[u] = opaque(qat[u] + bytes);
+    for (int u = 0; u < kQB; ++u) qat[u] = opaque(qat[u] + bytes);
   }
   template <int J, bool WHOLE>
   __device__ __forceinline__ void load(const PS& P, const QS& Q, int stage, int it, i32x4 pr,
@@ -761,7 +783,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void gated_kernel(
     if (t.e < 0) return;
     const int n0 = t.nt * kCols;
     const uint16_t* we = w + (int64_t(t.e) * 2 * I + n0) * H;
-    Side<true, S::BN, S::W, true> P;
+    Side<true, S::BN, S::W, true, S::kOnce> P;
     P.init_kc(we, we + int64_t(I) * H, H, H, I - n0);
     const uint16_t* xe = x + t.row0 * H;
     by_height<S>(t.rows, [&](auto mrep) {
@@ -797,7 +819,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void matmul_kernel(
     const int n0 = t.nt * S::BN;
     const uint16_t* we = w + (int64_t(t.e) * N + n0) * K;
     const uint16_t* xe = x + t.row0 * K;
-    Side<true, S::BN, S::W> P;
+    Side<true, S::BN, S::W, false, S::kOnce> P;
     P.init_kc(we, we, K, K, N - n0);
     by_height<S>(t.rows, [&](auto mrep) {
       constexpr int M = decltype(mrep)::value;
@@ -829,31 +851,39 @@ __global__ __launch_bounds__(S::kThreads, 2) void matmul_kernel(
   }
 }
 
-// dx = d W: the weights [N, K] are contiguous along the output's own index.
+// Tile number `id` of dx = d W: the weights [N, K] are contiguous along the output's own index.  False
+// behind the last tile.
+template <typename S>
+__device__ __forceinline__ bool data_grad_tile(uint32_t id, uint8_t* smem, const uint16_t* d,
+                                               const int32_t* off, const uint16_t* w, int64_t rows,
+                                               int E, int N, int K, uint16_t* dx) {
+  const Tile t = find_tile<S::FULL, S::BM, S::kThreads>(off, E, rows, (K + S::BN - 1) / S::BN, id);
+  if (t.e < 0) return false;
+  const int n0 = t.nt * S::BN;
+  const uint16_t* we = w + int64_t(t.e) * N * K + n0;
+  const uint16_t* de = d + t.row0 * N;
+  Side<false, S::BN, S::W, false, S::kOnce> P;
+  P.init_mc(we, K, N, n0);
+  by_height<S>(t.rows, [&](auto mrep) {
+    constexpr int M = decltype(mrep)::value;
+    Side<true, S::template kRows<M>, S::W> Q;
+    Q.init_kc(de, de, N, N, t.rows);
+    f32x4 acc[M][S::NR];
+    product<S, M>(acc, smem, P, Q, N);
+    each_row<S, false>(acc, smem, t.rows, [&](int m, int c, const f32x4(&v)[2]) {
+      if (n0 + c < K) store8(dx + (t.row0 + m) * K + n0 + c, v[0], v[1]);
+    });
+  });
+  return true;
+}
+
 template <typename S>
 __global__ __launch_bounds__(S::kThreads, 2) void data_grad_kernel(
     const uint16_t* d, const int32_t* off, const uint16_t* w, int64_t rows, int E, int N, int K,
     uint16_t* dx) {
   __shared__ __align__(1024) uint8_t smem[S::kLds];
-  const int ncol = (K + S::BN - 1) / S::BN;
-  for (uint32_t id = blockIdx.x;; id += gridDim.x) {
-    const Tile t = find_tile<S::FULL, S::BM, S::kThreads>(off, E, rows, ncol, id);
-    if (t.e < 0) return;
-    const int n0 = t.nt * S::BN;
-    const uint16_t* we = w + int64_t(t.e) * N * K + n0;
-    const uint16_t* de = d + t.row0 * N;
-    Side<false, S::BN, S::W> P;
-    P.init_mc(we, K, N, n0);
-    by_height<S>(t.rows, [&](auto mrep) {
-      constexpr int M = decltype(mrep)::value;
-      Side<true, S::template kRows<M>, S::W> Q;
-      Q.init_kc(de, de, N, N, t.rows);
-      f32x4 acc[M][S::NR];
-      product<S, M>(acc, smem, P, Q, N);
-      each_row<S, false>(acc, smem, t.rows, [&](int m, int c, const f32x4(&v)[2]) {
-        if (n0 + c < K) store8(dx + (t.row0 + m) * K + n0 + c, v[0], v[1]);
-      });
-    });
+  for (uint32_t id = blockIdx.x; data_grad_tile<S>(id, smem, d, off, w, rows, E, N, K, dx);
+       id += gridDim.x) {
   }
 }
 
@@ -941,43 +971,61 @@ __global__ __launch_bounds__(S::kThreads, 2) void weight_grad_kernel(
   stage_ready<0>();  // the loads behind the last tile
 }
 
-// The same, a block a tile.
+// One tile of the same, for a block of its own.
+template <typename S, bool F32>
+__device__ __forceinline__ void weight_grad_tile(uint32_t id, uint8_t* smem, const uint16_t* d,
+                                                 const uint16_t* x, const int32_t* off,
+                                                 int64_t rows, int E, int N, int K, void* dw) {
+  const uint32_t nn = (N + S::BM - 1) / S::BM, nk = (K + S::BN - 1) / S::BN;
+  const uint32_t seq = xcd_order(id, E * nn * nk);
+  const int e = int(seq / (nn * nk));
+  int mt, ct;
+  grid_order(seq - uint32_t(e) * nn * nk, nn, nk, mt, ct);
+  const int m0 = mt * S::BM, n0 = ct * S::BN;
+  int64_t lo, cnt;
+  expert_rows_scalar(off, e, rows, lo, cnt);
+  f32x4 acc[S::MR][S::NR] = {};
+  if (cnt > 0) {
+    Side<false, S::BN, S::W> P;
+    Side<false, S::BM, S::W> Q;
+    P.init_mc(x + lo * K + n0, K, cnt, n0);
+    Q.init_mc(d + lo * N + m0, N, cnt, m0);
+    product<S, S::MR>(acc, smem, P, Q, cnt);
+  }
+  each_row<S, false>(acc, smem, N - m0, [&](int m, int c, const f32x4(&v)[2]) {
+    if (n0 + c >= K) return;
+    const int64_t at = (int64_t(e) * N + m0 + m) * K + n0 + c;
+    if (F32) {
+      f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(dw) + at);
+      o[0] = v[0];
+      o[1] = v[1];
+    } else {
+      store8(static_cast<uint16_t*>(dw) + at, v[0], v[1]);
+    }
+  });
+}
+
+// Both gradients of a small product in one launch, a block a tile: the first `data_blocks` blocks
+// those of dx, the others those of dW.  Neither fills the chip, and each is over after one tile's time
+// (matmul_backward of 300 rows, 16 experts of 1288 x 520, with its elementwise part: 34.6 us with
+// a launch each, 23.9 with one).
+template <typename S, bool F32>
+__global__ __launch_bounds__(S::kThreads, 2) void both_grads_kernel(
+    const uint16_t* d, const uint16_t* x, const int32_t* off, const uint16_t* w, int64_t rows, int E,
+    int N, int K, uint32_t data_blocks, uint16_t* dx, void* dw) {
+  __shared__ __align__(1024) uint8_t smem[S::kLds];
+  if (blockIdx.x < data_blocks)
+    data_grad_tile<S>(blockIdx.x, smem, d, off, w, rows, E, N, K, dx);
+  else
+    weight_grad_tile<S, F32>(blockIdx.x - data_blocks, smem, d, x, off, rows, E, N, K, dw);
+}
+
 template <typename S, bool F32>
 __global__ __launch_bounds__(S::kThreads, 2) void weight_grad_alone_kernel(
     const uint16_t* d, const uint16_t* x, const int32_t* off, int64_t rows, int E, int N, int K,
     void* dw) {
   __shared__ __align__(1024) uint8_t smem[S::kLds];
-  const uint32_t nn = (N + S::BM - 1) / S::BM, nk = (K + S::BN - 1) / S::BN;
-  const uint32_t total = E * nn * nk;
-  for (uint32_t id = blockIdx.x; id < total; id += gridDim.x) {
-    const uint32_t seq = xcd_order(id, total);
-    const int e = int(seq / (nn * nk));
-    int mt, ct;
-    grid_order(seq - uint32_t(e) * nn * nk, nn, nk, mt, ct);
-    const int m0 = mt * S::BM, n0 = ct * S::BN;
-    int64_t lo, cnt;
-    expert_rows_scalar(off, e, rows, lo, cnt);
-    f32x4 acc[S::MR][S::NR] = {};
-    if (cnt > 0) {
-      Side<false, S::BN, S::W> P;
-      Side<false, S::BM, S::W> Q;
-      P.init_mc(x + lo * K + n0, K, cnt, n0);
-      Q.init_mc(d + lo * N + m0, N, cnt, m0);
-      product<S, S::MR>(acc, smem, P, Q, cnt);
-    }
-    each_row<S, false>(acc, smem, N - m0, [&](int m, int c, const f32x4(&v)[2]) {
-      if (n0 + c >= K) return;
-      const int64_t at = (int64_t(e) * N + m0 + m) * K + n0 + c;
-      if (F32) {
-        f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(dw) + at);
-        o[0] = v[0];
-        o[1] = v[1];
-      } else {
-        store8(static_cast<uint16_t*>(dw) + at, v[0], v[1]);
-      }
-    });
-    __syncthreads();  // every wave has read its sums before the next tile's loads arrive
-  }
+  weight_grad_tile<S, F32>(blockIdx.x, smem, d, x, off, rows, E, N, K, dw);
 }
 
 // ---------------------------------------------------------------------------
@@ -1121,9 +1169,14 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 bool bad_features(int32_t n) { return n < 8 || n > kMaxFeatures; }
 
 // One block of 8 waves a CU: two stages of 32 KiB of weights and up to 40 KiB of rows.
-using Tall = Shape<256, 288, 256, 2, 4, 144 * 1024>;
+template <bool ONCE>
+using TallOf = Shape<256, 288, 256, 2, 4, 144 * 1024, ONCE>;
+using Tall = TallOf<false>;
 using Square = Shape<256, 256, 256, 2, 4, 128 * 1024>;
-using Half = Shape<128, 128, 128, 2, 2, 72 * 1024>;  // 4 waves, two blocks a CU
+// 4 waves, two blocks a CU.
+template <bool ONCE>
+using HalfOf = Shape<128, 128, 128, 2, 2, 72 * 1024, ONCE>;
+using Half = HalfOf<false>;
 
 // The sizes every product shares; MOE_OK with rows == 0 allowed.  Tile numbers are 32-bit: what a
 // call could need at most has to stay below 2^31, far beyond any buffers that fit the card.
@@ -1156,6 +1209,26 @@ bool half_tiles(int64_t rows, int32_t E, int64_t cols) {
   return rows < int64_t(E) * 128 || row_tile_blocks(rows, E, Tall::FULL, cols) <= kCus / 2;
 }
 
+// Whether the weights [E, N, K] go past the caches: their strips are read by one tile each (no more
+// rows an expert than a tall tile holds), they are larger than the 256 MiB Infinity Cache, so that
+// nothing of them is there at the next call either, and their rows are whole lines, no part of which
+// is read again.  Kept against read once: 64 experts of 2048 x 4096 with 16 rows each 207 against 186
+// us, 256 rows 325 against 286, 512 rows 592 against 596; rows of 1000 features (8 experts of 7168)
+// 24 against 32 us.
+bool read_once(int64_t rows, int32_t E, int64_t N, int64_t K) {
+  return rows <= int64_t(E) * Tall::BM && E * N * K * 2 > int64_t(256) << 20 && K % 64 == 0;
+}
+
+// run(shape) of the shape a product with weights [E, N, K] takes; `per_tile`: those of the outputs'
+// `cols` columns that a tall tile covers.
+template <typename F>
+int with_shape(int64_t rows, int32_t E, int64_t N, int64_t K, int64_t cols, int per_tile, F run) {
+  const bool once = read_once(rows, E, N, K);
+  if (half_tiles(rows, E, (cols + per_tile - 1) / per_tile))
+    return once ? run(HalfOf<true>{}) : run(HalfOf<false>{});
+  return once ? run(TallOf<true>{}) : run(TallOf<false>{});
+}
+
 }  // namespace
 
 extern "C" {
@@ -1169,17 +1242,15 @@ int moe_expert_gated(const void* x, const int32_t* expert_offsets, const void* w
   if (!aligned(x, 16) || !aligned(w_gate_up, 16) || !aligned(h, 16) || !aligned(gate_up, 16) ||
       !aligned(expert_offsets, 4))
     return MOE_ERR_ALIGNMENT;
-  auto run = [&](auto shape, auto kern) {
+  return with_shape(rows, E, 2 * I, H, I, Tall::BN / 2, [&](auto shape) {
     using S = decltype(shape);
-    return launch(kern, row_tile_blocks(rows, E, S::FULL, (I + S::BN / 2 - 1) / (S::BN / 2)),
+    return launch(gated_kernel<S>,
+                  row_tile_blocks(rows, E, S::FULL, (I + S::BN / 2 - 1) / (S::BN / 2)),
                   S::kThreads, static_cast<hipStream_t>(stream),
                   static_cast<const uint16_t*>(x), expert_offsets,
                   static_cast<const uint16_t*>(w_gate_up), rows, E, H, I, act,
                   static_cast<uint16_t*>(h), static_cast<uint16_t*>(gate_up));
-  };
-  return half_tiles(rows, E, (I + Tall::BN / 2 - 1) / (Tall::BN / 2))
-             ? run(Half{}, gated_kernel<Half>)
-             : run(Tall{}, gated_kernel<Tall>);
+  });
 }
 
 int moe_expert_matmul(const void* x, const int32_t* expert_offsets, const void* w,
@@ -1191,51 +1262,56 @@ int moe_expert_matmul(const void* x, const int32_t* expert_offsets, const void* 
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(bias, 16) ||
       !aligned(residual, 16) || !aligned(pre, 16) || !aligned(expert_offsets, 4))
     return MOE_ERR_ALIGNMENT;
-  auto run = [&](auto shape, auto kern) {
+  return with_shape(rows, E, N, K, N, Tall::BN, [&](auto shape) {
     using S = decltype(shape);
-    return launch(kern, row_tile_blocks(rows, E, S::FULL, (N + S::BN - 1) / S::BN), S::kThreads,
-                  static_cast<hipStream_t>(stream), static_cast<const uint16_t*>(x),
+    return launch(matmul_kernel<S>, row_tile_blocks(rows, E, S::FULL, (N + S::BN - 1) / S::BN),
+                  S::kThreads, static_cast<hipStream_t>(stream), static_cast<const uint16_t*>(x),
                   expert_offsets, static_cast<const uint16_t*>(w),
                   static_cast<const uint16_t*>(bias), static_cast<const uint16_t*>(residual), rows,
                   E, K, N, act, static_cast<uint16_t*>(y), static_cast<uint16_t*>(pre));
-  };
-  return half_tiles(rows, E, (N + Tall::BN - 1) / Tall::BN)
-             ? run(Half{}, matmul_kernel<Half>)
-             : run(Tall{}, matmul_kernel<Tall>);
+  });
 }
 
-static int weight_grad(const void* d, const void* x, const int32_t* off, int64_t rows, int E,
-                       int N, int K, void* dw, int dw_f32, hipStream_t s) {
-  auto run = [&](auto shape, auto kern, int64_t most) {
-    using S = decltype(shape);
-    const int64_t n = int64_t(E) * ((N + S::BM - 1) / S::BM) * ((K + S::BN - 1) / S::BN);
-    return launch(kern, n < most ? n : most, S::kThreads, s, static_cast<const uint16_t*>(d),
-                  static_cast<const uint16_t*>(x), off, rows, E, N, K, dw);
+// dx = d W and dW = d^T x, either of which may be left out (NULL).
+static int product_grads(const void* d, const void* x, const int32_t* off, const void* w,
+                         int64_t rows, int E, int N, int K, void* dx, void* dw, int dw_f32,
+                         hipStream_t s) {
+  const uint16_t* dv = static_cast<const uint16_t*>(d);
+  const uint16_t* xv = static_cast<const uint16_t*>(x);
+  const uint16_t* wv = static_cast<const uint16_t*>(w);
+  uint16_t* dxv = static_cast<uint16_t*>(dx);
+  if (rows == 0) dx = nullptr;
+  auto tiles = [&](int side) {
+    return int64_t(E) * ((N + side - 1) / side) * ((K + side - 1) / side);
   };
   // So few square tiles that they fill the CUs once at best go in halves, a block each: 16 experts of
   // 1288 x 520 (288 square tiles) take 12.0 us in halves, 15.8 as square ones with a block each; 64 of
   // 2048 x 2048 take 123 us in one sequence of square tiles a CU, 152 with a block each, 173 in halves
   // (16 rows an expert), and 235, 260 and 310 us (256 rows).
-  const int64_t square = int64_t(E) * ((N + Square::BM - 1) / Square::BM) *
-                         ((K + Square::BN - 1) / Square::BN);
-  if (square <= kCus + kCus / 4)
-    return dw_f32 ? run(Half{}, weight_grad_alone_kernel<Half, true>, kMaxBlocks)
-                  : run(Half{}, weight_grad_alone_kernel<Half, false>, kMaxBlocks);
-  return dw_f32 ? run(Square{}, weight_grad_kernel<Square, true>, kCus)
-                : run(Square{}, weight_grad_kernel<Square, false>, kCus);
-}
-
-static int data_grad(const void* d, const int32_t* off, const void* w, int64_t rows, int E, int N,
-                     int K, void* dx, hipStream_t s) {
-  auto run = [&](auto shape, auto kern) {
-    using S = decltype(shape);
-    return launch(kern, row_tile_blocks(rows, E, S::FULL, (K + S::BN - 1) / S::BN), S::kThreads, s,
-                  static_cast<const uint16_t*>(d), off, static_cast<const uint16_t*>(w), rows, E, N,
-                  K, static_cast<uint16_t*>(dx));
-  };
-  return half_tiles(rows, E, (K + Tall::BN - 1) / Tall::BN)
-             ? run(Half{}, data_grad_kernel<Half>)
-             : run(Tall{}, data_grad_kernel<Tall>);
+  const bool halves = tiles(Square::BM) <= kCus + kCus / 4;
+  const int64_t data_cols = (K + Tall::BN - 1) / Tall::BN;
+  if (dx && dw && halves && half_tiles(rows, E, data_cols)) {
+    const int64_t nd = row_tile_blocks(rows, E, Half::FULL, (K + Half::BN - 1) / Half::BN);
+    const int64_t n = nd + tiles(Half::BM);
+    if (n <= kMaxBlocks)
+      return launch(dw_f32 ? both_grads_kernel<Half, true> : both_grads_kernel<Half, false>, n,
+                    Half::kThreads, s, dv, xv, off, wv, rows, E, N, K, uint32_t(nd), dxv, dw);
+  }
+  int st = MOE_OK;
+  if (dx)
+    st = with_shape(rows, E, N, K, K, Tall::BN, [&](auto shape) {
+      using S = decltype(shape);
+      return launch(data_grad_kernel<S>, row_tile_blocks(rows, E, S::FULL, (K + S::BN - 1) / S::BN),
+                    S::kThreads, s, dv, off, wv, rows, E, N, K, dxv);
+    });
+  if (st != MOE_OK || !dw) return st;
+  if (halves)
+    return launch(
+        dw_f32 ? weight_grad_alone_kernel<Half, true> : weight_grad_alone_kernel<Half, false>,
+        tiles(Half::BM), Half::kThreads, s, dv, xv, off, rows, E, N, K, dw);
+  const int64_t n = tiles(Square::BM);
+  return launch(dw_f32 ? weight_grad_kernel<Square, true> : weight_grad_kernel<Square, false>,
+                n < kCus ? n : kCus, Square::kThreads, s, dv, xv, off, rows, E, N, K, dw);
 }
 
 int moe_expert_gated_backward(const void* dh, const void* gate_up, const void* x,
@@ -1258,12 +1334,9 @@ int moe_expert_gated_backward(const void* dh, const void* gate_up, const void* x
     st = launch(gated_grad_kernel, (rows * (I / 8) + 255) / 256, 256, s,
                 static_cast<const uint16_t*>(dh), static_cast<const uint16_t*>(gate_up),
                 expert_offsets, rows, E, I, act, static_cast<uint16_t*>(dgate_up));
-    if (st == MOE_OK && dx)
-      st = data_grad(dgate_up, expert_offsets, w_gate_up, rows, E, 2 * I, H, dx, s);
   }
-  if (st == MOE_OK && dw)
-    st = weight_grad(dgate_up, x, expert_offsets, rows, E, 2 * I, H, dw, dw_f32, s);
-  return st;
+  if (st != MOE_OK) return st;
+  return product_grads(dgate_up, x, expert_offsets, w_gate_up, rows, E, 2 * I, H, dx, dw, dw_f32, s);
 }
 
 int moe_expert_matmul_backward(const void* dy, const void* pre, const void* x,
@@ -1290,9 +1363,8 @@ int moe_expert_matmul_backward(const void* dy, const void* pre, const void* x,
                 expert_offsets, rows, E, N, act,
                 has_act ? static_cast<uint16_t*>(dpre) : nullptr, dbias);
   }
-  if (st == MOE_OK && dx && rows > 0) st = data_grad(d, expert_offsets, w, rows, E, N, K, dx, s);
-  if (st == MOE_OK && dw) st = weight_grad(d, x, expert_offsets, rows, E, N, K, dw, dw_f32, s);
-  return st;
+  if (st != MOE_OK) return st;
+  return product_grads(d, x, expert_offsets, w, rows, E, N, K, dx, dw, dw_f32, s);
 }
 
 int moe_combine_backward(const void* dout, const void* y, const int32_t* pair_row,
