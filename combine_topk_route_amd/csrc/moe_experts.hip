@@ -94,31 +94,43 @@ __device__ __forceinline__ float normal_cdf(float z, float& e) {
   return z < 0.f ? tail : 1.0f - tail;
 }
 
-__device__ __forceinline__ float act_value(float z, int act) {
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
   float e;
-  switch (act) {
-    case MOE_ACT_SILU: return z * sigmoid(z);
-    case MOE_ACT_GELU: return z * normal_cdf(z, e);
-    case MOE_ACT_RELU: return z < 0.f ? 0.f : z;  // a NaN stays one
-    default: return z;
-  }
+  if constexpr (ACT == MOE_ACT_SILU) return z * sigmoid(z);
+  if constexpr (ACT == MOE_ACT_GELU) return z * normal_cdf(z, e);
+  if constexpr (ACT == MOE_ACT_RELU) return z < 0.f ? 0.f : z;  // a NaN stays one
+  return z;
 }
 
 // d act / dz (relu's is 0 at 0).
-__device__ __forceinline__ float act_slope(float z, int act) {
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
   float e;
-  switch (act) {
-    case MOE_ACT_SILU: {
-      const float s = sigmoid(z);
-      return s * (1.f + z * (1.f - s));
-    }
-    case MOE_ACT_GELU: {
-      const float phi = normal_cdf(z, e);
-      return __builtin_fmaf(z * e, kInvSqrt2Pi, phi);
-    }
-    case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
-    default: return 1.f;
+  if constexpr (ACT == MOE_ACT_SILU) {
+    const float s = sigmoid(z);
+    return s * (1.f + z * (1.f - s));
   }
+  if constexpr (ACT == MOE_ACT_GELU) {
+    const float phi = normal_cdf(z, e);
+    return __builtin_fmaf(z * e, kInvSqrt2Pi, phi);
+  }
+  if constexpr (ACT == MOE_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+  return 1.f;
+}
+
+// f(integral_constant<int, act>): one branch in front of a loop over rows, whose code is then one
+// short piece.  With the branch inside, a tile's epilogue took 7 us longer, mostly to fetch it.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  if (act == MOE_ACT_SILU)
+    f(std::integral_constant<int, MOE_ACT_SILU>{});
+  else if (act == MOE_ACT_GELU)
+    f(std::integral_constant<int, MOE_ACT_GELU>{});
+  else if (act == MOE_ACT_RELU)
+    f(std::integral_constant<int, MOE_ACT_RELU>{});
+  else
+    f(std::integral_constant<int, MOE_ACT_NONE>{});
 }
 
 // ---------------------------------------------------------------------------
@@ -687,9 +699,10 @@ __device__ __forceinline__ void load8(const uint16_t* p, f32x4& a, f32x4& b) {
   b = f32x4{bf16_lo(v[2]), bf16_hi(v[2]), bf16_lo(v[3]), bf16_hi(v[3])};
 }
 
-__device__ __forceinline__ f32x4 act4(f32x4 v, int act) {
+template <int ACT>
+__device__ __forceinline__ f32x4 act4(f32x4 v) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = act_value(v[i], act);
+  for (int i = 0; i < 4; ++i) v[i] = act_value<ACT>(v[i]);
   return v;
 }
 
@@ -792,15 +805,18 @@ __global__ __launch_bounds__(S::kThreads, 2) void gated_kernel(
       Q.init_kc(xe, xe, H, H, t.rows);
       f32x4 acc[M][S::NR];
       product<S, M>(acc, smem, P, Q, H);
-      each_row<S, true>(acc, smem, t.rows, [&](int m, int c, const f32x4(&v)[4]) {
-        const int n = n0 + c;
-        if (n >= I) return;
-        const int64_t row = t.row0 + m;
-        store8(h + row * I + n, act4(v[0], act) * v[2], act4(v[1], act) * v[3]);
-        if (gu != nullptr) {
-          store8(gu + row * 2 * I + n, v[0], v[1]);
-          store8(gu + row * 2 * I + I + n, v[2], v[3]);
-        }
+      with_act(act, [&](auto a) {
+        if constexpr (a != MOE_ACT_NONE)
+          each_row<S, true>(acc, smem, t.rows, [&](int m, int c, const f32x4(&v)[4]) {
+            const int n = n0 + c;
+            if (n >= I) return;
+            const int64_t row = t.row0 + m;
+            store8(h + row * I + n, act4<a>(v[0]) * v[2], act4<a>(v[1]) * v[3]);
+            if (gu != nullptr) {
+              store8(gu + row * 2 * I + n, v[0], v[1]);
+              store8(gu + row * 2 * I + I + n, v[2], v[3]);
+            }
+          });
       });
     });
   }
@@ -827,25 +843,27 @@ __global__ __launch_bounds__(S::kThreads, 2) void matmul_kernel(
       Q.init_kc(xe, xe, K, K, t.rows);
       f32x4 acc[M][S::NR];
       product<S, M>(acc, smem, P, Q, K);
-      each_row<S, false>(acc, smem, t.rows, [&](int m, int c, const f32x4(&v)[2]) {
-        const int n = n0 + c;
-        if (n >= N) return;
-        const int64_t at = (t.row0 + m) * N + n;
-        f32x4 v0 = v[0], v1 = v[1], r0, r1;
-        if (bias != nullptr) {
-          load8(bias + int64_t(t.e) * N + n, r0, r1);
-          v0 += r0;
-          v1 += r1;
-        }
-        if (pre != nullptr) store8(pre + at, v0, v1);
-        v0 = act4(v0, act);
-        v1 = act4(v1, act);
-        if (res != nullptr) {
-          load8(res + at, r0, r1);
-          v0 += r0;
-          v1 += r1;
-        }
-        store8(y + at, v0, v1);
+      with_act(act, [&](auto a) {
+        each_row<S, false>(acc, smem, t.rows, [&](int m, int c, const f32x4(&v)[2]) {
+          const int n = n0 + c;
+          if (n >= N) return;
+          const int64_t at = (t.row0 + m) * N + n;
+          f32x4 v0 = v[0], v1 = v[1], r0, r1;
+          if (bias != nullptr) {
+            load8(bias + int64_t(t.e) * N + n, r0, r1);
+            v0 += r0;
+            v1 += r1;
+          }
+          if (pre != nullptr) store8(pre + at, v0, v1);
+          v0 = act4<a>(v0);
+          v1 = act4<a>(v1);
+          if (res != nullptr) {
+            load8(res + at, r0, r1);
+            v0 += r0;
+            v1 += r1;
+          }
+          store8(y + at, v0, v1);
+        });
       });
     });
   }
@@ -1033,9 +1051,10 @@ __global__ __launch_bounds__(S::kThreads, 2) void weight_grad_alone_kernel(
 // ---------------------------------------------------------------------------
 
 // [dg du] from dh and the kept factors, 8 columns per thread.
+template <int ACT>
 __global__ __launch_bounds__(256) void gated_grad_kernel(const uint16_t* dh, const uint16_t* gu,
                                                          const int32_t* off, int64_t rows, int E,
-                                                         int I, int act, uint16_t* dgu) {
+                                                         int I, uint16_t* dgu) {
   const int64_t first = off[0] < 0 ? 0 : (off[0] > rows ? rows : off[0]);
   const int64_t last = off[E] < 0 ? 0 : (off[E] > rows ? rows : off[E]);
   const int C = I / 8;
@@ -1052,9 +1071,9 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(const uint16_t* dh, con
     for (int q = 0; q < 4; ++q) {
       const float h0 = bf16_lo(vh[q]), h1 = bf16_hi(vh[q]);
       const float g0 = bf16_lo(vg[q]), g1 = bf16_hi(vg[q]);
-      og[q] = pack_bf16x2(h0 * bf16_lo(vu[q]) * act_slope(g0, act),
-                          h1 * bf16_hi(vu[q]) * act_slope(g1, act));
-      ou[q] = pack_bf16x2(h0 * act_value(g0, act), h1 * act_value(g1, act));
+      og[q] = pack_bf16x2(h0 * bf16_lo(vu[q]) * act_slope<ACT>(g0),
+                          h1 * bf16_hi(vu[q]) * act_slope<ACT>(g1));
+      ou[q] = pack_bf16x2(h0 * act_value<ACT>(g0), h1 * act_value<ACT>(g1));
     }
     *reinterpret_cast<u32x4*>(dgu + row * 2 * I + c) = og;
     *reinterpret_cast<u32x4*>(dgu + row * 2 * I + I + c) = ou;
@@ -1064,9 +1083,10 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(const uint16_t* dh, con
 // dpre = dy * act'(pre) and dbias[e] = its sum over the expert's rows, in a
 // fixed order: a block owns 64 columns of one expert, 32 threads a column
 // chunk, each adding every 32nd row.
+template <int ACT>
 __global__ __launch_bounds__(256) void pre_grad_kernel(const uint16_t* dy, const uint16_t* pre,
                                                        const int32_t* off, int64_t rows, int E,
-                                                       int N, int act, uint16_t* dpre,
+                                                       int N, uint16_t* dpre,
                                                        float* dbias) {
   __shared__ float part[32][65];
   const int64_t strips = (N + 63) / 64;
@@ -1081,11 +1101,11 @@ __global__ __launch_bounds__(256) void pre_grad_kernel(const uint16_t* dy, const
         const int64_t at = (lo + r) * N + c;
         const u32x4 vy = *reinterpret_cast<const u32x4*>(dy + at);
         u32x4 vp = {0u, 0u, 0u, 0u}, o;
-        if (act != MOE_ACT_NONE) vp = *reinterpret_cast<const u32x4*>(pre + at);
+        if (ACT != MOE_ACT_NONE) vp = *reinterpret_cast<const u32x4*>(pre + at);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float d0 = bf16_lo(vy[q]) * act_slope(bf16_lo(vp[q]), act);
-          const float d1 = bf16_hi(vy[q]) * act_slope(bf16_hi(vp[q]), act);
+          const float d0 = bf16_lo(vy[q]) * act_slope<ACT>(bf16_lo(vp[q]));
+          const float d1 = bf16_hi(vy[q]) * act_slope<ACT>(bf16_hi(vp[q]));
           sum[2 * q] += d0;
           sum[2 * q + 1] += d1;
           o[q] = pack_bf16x2(d0, d1);
@@ -1201,12 +1221,15 @@ int64_t row_tile_blocks(int64_t rows, int32_t E, int bm, int64_t cols) {
 
 // Whether a product over the experts' rows takes Half tiles: under 128 rows an expert (the tall
 // tiles' heights are then mostly empty, and two blocks a CU cover each other's waits), or so few tall
-// tiles that half of the CUs would have none.  `cols`: outputs to a tall tile's row.
+// tiles that half of the CUs would have none.  `per_tile`: those of the outputs' `cols` columns that a
+// tall tile covers.
 // Measured, rows spread at random, tall against half tiles: 64 experts of 2048 x 2048, 64 rows each,
 // 142 against 127 us, 128 rows 153 against 158, 256 rows 183 against 212; 16 of 4096 x 4096, 64 rows
-// 134 against 116, 128 rows 146 against 179; 8 of 520 x 1280, 512 rows 30 against 19.
-bool half_tiles(int64_t rows, int32_t E, int64_t cols) {
-  return rows < int64_t(E) * 128 || row_tile_blocks(rows, E, Tall::FULL, cols) <= kCus / 2;
+// 134 against 116, 128 rows 146 against 179; 8 of 520 x 1280, 512 rows 30 against 19; 8 of 2048 x 544
+// (3 column tiles, 7 blocks in 8 idle), 512 rows 47 against 26.
+bool half_tiles(int64_t rows, int32_t E, int64_t cols, int per_tile) {
+  return rows < int64_t(E) * 128 ||
+         row_tile_blocks(rows, E, Tall::FULL, (cols + per_tile - 1) / per_tile) <= kCus / 2;
 }
 
 // Whether the weights [E, N, K] go past the caches: their strips are read by one tile each (no more
@@ -1219,12 +1242,11 @@ bool read_once(int64_t rows, int32_t E, int64_t N, int64_t K) {
   return rows <= int64_t(E) * Tall::BM && E * N * K * 2 > int64_t(256) << 20 && K % 64 == 0;
 }
 
-// run(shape) of the shape a product with weights [E, N, K] takes; `per_tile`: those of the outputs'
-// `cols` columns that a tall tile covers.
+// run(shape) of the shape a product with weights [E, N, K] takes.
 template <typename F>
 int with_shape(int64_t rows, int32_t E, int64_t N, int64_t K, int64_t cols, int per_tile, F run) {
   const bool once = read_once(rows, E, N, K);
-  if (half_tiles(rows, E, (cols + per_tile - 1) / per_tile))
+  if (half_tiles(rows, E, cols, per_tile))
     return once ? run(HalfOf<true>{}) : run(HalfOf<false>{});
   return once ? run(TallOf<true>{}) : run(TallOf<false>{});
 }
@@ -1289,8 +1311,7 @@ static int product_grads(const void* d, const void* x, const int32_t* off, const
   // 2048 x 2048 take 123 us in one sequence of square tiles a CU, 152 with a block each, 173 in halves
   // (16 rows an expert), and 235, 260 and 310 us (256 rows).
   const bool halves = tiles(Square::BM) <= kCus + kCus / 4;
-  const int64_t data_cols = (K + Tall::BN - 1) / Tall::BN;
-  if (dx && dw && halves && half_tiles(rows, E, data_cols)) {
+  if (dx && dw && halves && half_tiles(rows, E, K, Tall::BN)) {
     const int64_t nd = row_tile_blocks(rows, E, Half::FULL, (K + Half::BN - 1) / Half::BN);
     const int64_t n = nd + tiles(Half::BM);
     if (n <= kMaxBlocks)
@@ -1331,9 +1352,12 @@ int moe_expert_gated_backward(const void* dh, const void* gate_up, const void* x
     return MOE_ERR_ALIGNMENT;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (rows > 0) {
-    st = launch(gated_grad_kernel, (rows * (I / 8) + 255) / 256, 256, s,
+    auto kern = act == MOE_ACT_SILU   ? gated_grad_kernel<MOE_ACT_SILU>
+                : act == MOE_ACT_GELU ? gated_grad_kernel<MOE_ACT_GELU>
+                                      : gated_grad_kernel<MOE_ACT_RELU>;
+    st = launch(kern, (rows * (I / 8) + 255) / 256, 256, s,
                 static_cast<const uint16_t*>(dh), static_cast<const uint16_t*>(gate_up),
-                expert_offsets, rows, E, I, act, static_cast<uint16_t*>(dgate_up));
+                expert_offsets, rows, E, I, static_cast<uint16_t*>(dgate_up));
   }
   if (st != MOE_OK) return st;
   return product_grads(dgate_up, x, expert_offsets, w_gate_up, rows, E, 2 * I, H, dx, dw, dw_f32, s);
@@ -1358,9 +1382,13 @@ int moe_expert_matmul_backward(const void* dy, const void* pre, const void* x,
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const void* d = has_act ? dpre : dy;
   if ((has_act && rows > 0) || dbias) {
-    st = launch(pre_grad_kernel, int64_t(E) * ((N + 63) / 64), 256, s,
+    auto kern = act == MOE_ACT_SILU   ? pre_grad_kernel<MOE_ACT_SILU>
+                : act == MOE_ACT_GELU ? pre_grad_kernel<MOE_ACT_GELU>
+                : act == MOE_ACT_RELU ? pre_grad_kernel<MOE_ACT_RELU>
+                                      : pre_grad_kernel<MOE_ACT_NONE>;
+    st = launch(kern, int64_t(E) * ((N + 63) / 64), 256, s,
                 static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(pre),
-                expert_offsets, rows, E, N, act,
+                expert_offsets, rows, E, N,
                 has_act ? static_cast<uint16_t*>(dpre) : nullptr, dbias);
   }
   if (st != MOE_OK) return st;
