@@ -329,3 +329,107 @@ def test_repeated_calls_give_the_same_bits():
         if first is not None:
             assert all(torch.equal(a, b) for a, b in zip(first, got))
         first = got
+
+
+# Rows for tall tiles: every height, both sides of 256 and 288, spread over two and three tiles.
+TALL = [257, 288, 289, 255, 600, 1, 0, 700, 33, 64, 96, 161]
+
+
+def assert_rows_written(t, sp, mark):
+    inside = fill(t.clone(), sp, 0)
+    assert bool((t[~inside] == mark).all()), "rows outside the experts were written"
+
+
+@pytest.mark.parametrize("K", [72, 64, 520])
+def test_tall_tiles_exact(K):
+    """Enough rows and outputs for the tall tiles, forward and data gradient."""
+    g = gen(12)
+    N = 4112
+    P, E, sp = rows_of(TALL), len(TALL), spans(TALL, PAD)
+    off = offsets_of(TALL, PAD)
+    x, w, dy = ints(g, -2, 2, P, K), ints(g, -2, 2, E, N, K), ints(g, -2, 2, P, K)
+    inside = fill(x, sp, float("nan"))
+    y = torch.full((P, N), 77.0, dtype=BF, device=DEV)
+    moe.moe_expert_matmul(x, off, w, y=y)
+    x0 = torch.where(inside[:, None], x, 0)
+    want, _ = product64(x0, w, sp)
+    assert_bits(y[inside], want[inside], "y")
+    assert_rows_written(y, sp, 77)
+    # the data gradient of a product with K outputs and N inputs
+    wt = w.transpose(1, 2).contiguous()
+    dx = torch.full((P, N), 77.0, dtype=BF, device=DEV)
+    fill(dy, sp, float("inf"))
+    moe.moe_expert_matmul_backward(dy, torch.zeros((P, N), dtype=BF, device=DEV), off, wt, dx=dx,
+                                   need_dw=False)
+    want, _ = product64(torch.where(inside[:, None], dy, 0), w, sp)
+    assert_bits(dx[inside], want[inside], "dx")
+    assert_rows_written(dx, sp, 77)
+    # the gated block: N = 2 I, |gate| and |up| at most 2 K, their product below 2^24
+    z, _ = product64(torch.clamp(x0, -1, 1), w, sp)
+    h, gu = moe.moe_expert_gated(x.clamp(-1, 1), off, w, act="relu", save_gate_up=True)
+    assert_bits(gu[inside], z[inside], "gate_up")
+    assert_bits(h[inside], (z[:, :N // 2].clamp(min=0) * z[:, N // 2:])[inside], "h")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_tall_tiles_epilogue(act):
+    g = gen(13)
+    K, N = 136, 4112
+    P, E, sp = rows_of(TALL), len(TALL), spans(TALL, PAD)
+    off = offsets_of(TALL, PAD)
+    x, w = normal(g, P, K), normal(g, E, N, K, scale=K**-0.5)
+    bias, res = normal(g, E, N), normal(g, P, N)
+    y, pre = moe.moe_expert_matmul(x, off, w, bias=bias, act=act, residual=res, save_pre=True)
+    z, mag = product64(x, w, sp)
+    inside = fill(x.clone(), sp, 0)
+    for e, a, b in sp:
+        z[a:b] += bias[e].double()
+    zerr = (K + 1) * 2.0**-23 * (mag + bias.double().abs().max())
+    assert_within(pre[inside], z[inside], (HALF * z.abs() + zerr)[inside], "pre")
+    want = act64(z, act) + res.double()
+    tol = HALF * want.abs() + 1.22 * zerr + 2.0**-18 * (z.abs() + 1)
+    assert_within(y[inside], want[inside], tol[inside], "y")
+    over = res.clone()
+    moe.moe_expert_matmul(x, off, w, bias=bias, act=act, residual=over, y=over)
+    assert torch.equal(over[inside], y[inside]) and torch.equal(over[~inside], res[~inside])
+
+
+# One sequence of tiles a CU: lengths from no stage to several, tiles of the same expert apart.
+SEQUENCE = [0, 1, 63, 64, 65, 0, 0, 128, 129, 700, 5, 0, 191, 192, 193, 2, 300, 31, 32, 0, 77, 256, 1, 0]
+
+
+@pytest.mark.parametrize("N,K", [(1032, 776), (1288, 1160)])
+@pytest.mark.parametrize("counts", [SEQUENCE, [0] * 23 + [9], [0] * 24], ids=["mixed", "one", "none"])
+def test_weight_gradient_sequences(N, K, counts):
+    g = gen(14)
+    P, E, sp = rows_of(counts), len(counts), spans(counts, PAD)
+    off = offsets_of(counts, PAD)
+    x, d, w = ints(g, -2, 2, P, K), ints(g, -2, 2, P, N), torch.zeros((E, N, K), dtype=BF, device=DEV)
+    inside = fill(x, sp, float("nan"))
+    fill(d, sp, float("inf"))
+    want, _ = weight64(torch.where(inside[:, None], d, 0), torch.where(inside[:, None], x, 0), sp, E)
+    for dtype in (BF, torch.float32):
+        dw = torch.full((E, N, K), 77.0, dtype=dtype, device=DEV)
+        moe.moe_expert_matmul_backward(d, x, off, w, dw=dw, need_dx=False)
+        assert_bits(dw, want, f"dw as {dtype}")
+
+
+@pytest.mark.parametrize("per", [5, 200])
+def test_weights_beyond_the_cache(per):
+    """Weights over 256 MiB, which go past the caches: few rows an expert and about a tall tile's."""
+    g = gen(15)
+    E, N, K = 64, 2048, 1088
+    counts = [(per + 37 * e) % (2 * per + 1) for e in range(E)]
+    P, sp = rows_of(counts), spans(counts, PAD)
+    off = offsets_of(counts, PAD)
+    x, w, d = ints(g, -1, 1, P, K), ints(g, -2, 2, E, N, K), ints(g, -2, 2, P, N)
+    inside = fill(x, sp, float("nan"))
+    x0 = torch.where(inside[:, None], x, 0)
+    z, _ = product64(x0, w, sp)
+    y, _ = moe.moe_expert_matmul(x, off, w)
+    assert_bits(y[inside], z[inside], "y")
+    _, gu = moe.moe_expert_gated(x, off, w, save_gate_up=True)
+    assert_bits(gu[inside], z[inside], "gate_up")
+    r = moe.moe_expert_matmul_backward(d, x, off, w, need_dw=False)
+    want, _ = product64(torch.where(inside[:, None], d, 0), w.transpose(1, 2), sp)
+    assert_bits(r.dx[inside], want[inside], "dx")
