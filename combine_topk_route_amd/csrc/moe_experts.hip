@@ -699,6 +699,14 @@ __device__ __forceinline__ void load8(const uint16_t* p, f32x4& a, f32x4& b) {
   b = f32x4{bf16_lo(v[2]), bf16_hi(v[2]), bf16_lo(v[3]), bf16_hi(v[3])};
 }
 
+__device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
+  *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+__device__ __forceinline__ f32x4 load4(const uint16_t* p) {
+  const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+  return f32x4{bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1])};
+}
+
 template <int ACT>
 __device__ __forceinline__ f32x4 act4(f32x4 v) {
 #pragma unroll
@@ -866,6 +874,103 @@ __global__ __launch_bounds__(S::kThreads, 2) void matmul_kernel(
         });
       });
     });
+  }
+}
+
+// The forward products where few rows meet few outputs: 32 rows by 32 positions (gated: 16 gate
+// columns and the same 16 up columns) a block, the inner axis split over its 8 waves.  Each wave takes
+// every 8th piece of 32 k straight from memory into the matrix instruction's registers, kAhead pieces
+// at a time; the 8 partial sums meet in LDS and are added in the waves' order.  With a few blocks on
+// the chip the time is that of one block, and what bounds it is how often a wave waits for memory: 8
+// waves of 4 pieces wait once per 1024 k, where a wave of the 128x128 tiles does per 64.
+constexpr int kThinRows = 32, kThinCols = 32, kThinWaves = 8;
+
+template <bool GATED>
+__global__ __launch_bounds__(kThinWaves * kWave) void thin_kernel(
+    const uint16_t* x, const int32_t* off, const uint16_t* w, const uint16_t* bias,
+    const uint16_t* res, int64_t rows, int E, int K, int N, int act, uint16_t* y, uint16_t* pre) {
+  constexpr int kAhead = 4, kCols = GATED ? kThinCols / 2 : kThinCols;
+  __shared__ f32x4 part[kThinWaves][4][kWave];
+  const int ncol = (N + kCols - 1) / kCols;
+  const int wv = wave_id(), l = lane_id(), i = l % 16, q = l / 16;
+  for (uint32_t id = blockIdx.x;; id += gridDim.x) {
+    const Tile t = find_tile<kThinRows, kThinRows, kThinWaves * kWave>(off, E, rows, ncol, id);
+    if (t.e < 0) return;
+    const int n0 = t.nt * kCols;
+    // Rows and columns outside the tile repeat its last one; their sums are not stored.
+    const uint16_t *wp[2], *xp[2];
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      const int n = n0 + (GATED ? 0 : f * 16) + i, m = f * 16 + i;
+      wp[f] = w + (int64_t(t.e) * (GATED ? 2 : 1) * N + (GATED ? f * int64_t(N) : 0) +
+                   (n < N ? n : N - 1)) * K + q * 8;
+      xp[f] = x + (t.row0 + (m < t.rows ? m : t.rows - 1)) * K + q * 8;
+    }
+    f32x4 acc[2][2] = {};
+    for (int k0 = wv * 32; k0 < K; k0 += kThinWaves * 32 * kAhead) {
+      u32x4 a[kAhead][2], b[kAhead][2];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int k = k0 + u * kThinWaves * 32;
+        const bool in = k + q * 8 < K;
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          a[u][f] = b[u][f] = u32x4{0u, 0u, 0u, 0u};
+          if (in) {
+            a[u][f] = *reinterpret_cast<const u32x4*>(wp[f] + k);
+            b[u][f] = *reinterpret_cast<const u32x4*>(xp[f] + k);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            acc[f][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8, a[u][f]), __builtin_bit_cast(bf16x8, b[u][m]),
+                acc[f][m], 0, 0, 0);
+    }
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) part[wv][f * 2 + m][l] = acc[f][m];
+    __syncthreads();
+    // waves 0 and 1 finish the two row fragments (gated: both factors), or waves 0 to 3 a fragment each
+    const int m = wv % 2 * 16 + i;
+    if (wv < (GATED ? 2 : 4) && m < t.rows) {
+      auto sum = [&](int f) {
+        f32x4 v = part[0][f * 2 + wv % 2][l];
+#pragma unroll
+        for (int s = 1; s < kThinWaves; ++s) v += part[s][f * 2 + wv % 2][l];
+        return v;
+      };
+      const int64_t row = t.row0 + m;
+      if constexpr (GATED) {
+        const int n = n0 + q * 4;
+        const f32x4 g = sum(0), u = sum(1);
+        if (n < N) {
+          with_act(act, [&](auto c) { store4(y + row * N + n, act4<c>(g) * u); });
+          if (pre != nullptr) {
+            store4(pre + row * 2 * N + n, g);
+            store4(pre + row * 2 * N + N + n, u);
+          }
+        }
+      } else {
+        const int n = n0 + wv / 2 * 16 + q * 4;
+        f32x4 v = sum(wv / 2);
+        if (n < N) {
+          const int64_t at = row * N + n;
+          if (bias != nullptr) v += load4(bias + int64_t(t.e) * N + n);
+          if (pre != nullptr) store4(pre + at, v);
+          with_act(act, [&](auto c) { v = act4<c>(v); });
+          if (res != nullptr) v += load4(res + at);
+          store4(y + at, v);
+        }
+      }
+    }
+    __syncthreads();  // part may be written again
   }
 }
 
@@ -1242,6 +1347,18 @@ bool read_once(int64_t rows, int32_t E, int64_t N, int64_t K) {
   return rows <= int64_t(E) * Tall::BM && E * N * K * 2 > int64_t(256) << 20 && K % 64 == 0;
 }
 
+// Whether a forward product goes to thin_kernel: no more than 32 rows an expert, and too few half tiles
+// for one on each CU (`per_half`: the outputs' columns that one covers).  Measured, half tiles against
+// thin ones, rows spread at random: 16 experts of 128 x 2312 (20 half tiles) 512 rows 15.3 against 9.4
+// us; 2 of 3504 x 3256 (28) one row 16.0 against 9.5, (56) 64 rows 23.8 against 21.2; 8 of 1024 x 512
+// (64) 32 rows 7.0 against 7.3; 16 of 4096 x 4096 (64) 2 rows 29.3 against 13.9; 64 of 2048 x 1024 (128)
+// 8 rows 8.9 against 8.6, (256) 16 rows 12.2 against 15.8; 8 of 7168 x 1000 (448) 8 rows 18.9 against
+// 21.1; 16 of 4096 x 4096 (512) 32 rows 78 against 87.
+bool thin_tiles(int64_t rows, int32_t E, int64_t cols, int per_half) {
+  return rows <= int64_t(E) * kThinRows &&
+         row_tile_blocks(rows, E, Half::FULL, (cols + per_half - 1) / per_half) < kCus;
+}
+
 // run(shape) of the shape a product with weights [E, N, K] takes.
 template <typename F>
 int with_shape(int64_t rows, int32_t E, int64_t N, int64_t K, int64_t cols, int per_tile, F run) {
@@ -1264,6 +1381,13 @@ int moe_expert_gated(const void* x, const int32_t* expert_offsets, const void* w
   if (!aligned(x, 16) || !aligned(w_gate_up, 16) || !aligned(h, 16) || !aligned(gate_up, 16) ||
       !aligned(expert_offsets, 4))
     return MOE_ERR_ALIGNMENT;
+  if (thin_tiles(rows, E, I, Half::BN / 2))
+    return launch(thin_kernel<true>,
+                  row_tile_blocks(rows, E, kThinRows, (I + kThinCols / 2 - 1) / (kThinCols / 2)),
+                  kThinWaves * kWave, static_cast<hipStream_t>(stream),
+                  static_cast<const uint16_t*>(x), expert_offsets,
+                  static_cast<const uint16_t*>(w_gate_up), nullptr, nullptr, rows, E, H, I, act,
+                  static_cast<uint16_t*>(h), static_cast<uint16_t*>(gate_up));
   return with_shape(rows, E, 2 * I, H, I, Tall::BN / 2, [&](auto shape) {
     using S = decltype(shape);
     return launch(gated_kernel<S>,
@@ -1284,6 +1408,14 @@ int moe_expert_matmul(const void* x, const int32_t* expert_offsets, const void* 
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(bias, 16) ||
       !aligned(residual, 16) || !aligned(pre, 16) || !aligned(expert_offsets, 4))
     return MOE_ERR_ALIGNMENT;
+  if (thin_tiles(rows, E, N, Half::BN))
+    return launch(thin_kernel<false>,
+                  row_tile_blocks(rows, E, kThinRows, (N + kThinCols - 1) / kThinCols),
+                  kThinWaves * kWave, static_cast<hipStream_t>(stream),
+                  static_cast<const uint16_t*>(x), expert_offsets,
+                  static_cast<const uint16_t*>(w), static_cast<const uint16_t*>(bias),
+                  static_cast<const uint16_t*>(residual), rows, E, K, N, act,
+                  static_cast<uint16_t*>(y), static_cast<uint16_t*>(pre));
   return with_shape(rows, E, N, K, N, Tall::BN, [&](auto shape) {
     using S = decltype(shape);
     return launch(matmul_kernel<S>, row_tile_blocks(rows, E, S::FULL, (N + S::BN - 1) / S::BN),

@@ -433,3 +433,64 @@ def test_weights_beyond_the_cache(per):
     r = moe.moe_expert_matmul_backward(d, x, off, w, need_dw=False)
     want, _ = product64(torch.where(inside[:, None], d, 0), w.transpose(1, 2), sp)
     assert_bits(r.dx[inside], want[inside], "dx")
+
+
+# Few rows and few outputs, where a block's waves share the inner axis: runs around a tile's 32 rows,
+# all rows at one expert of many, one row each.
+FEW = {
+    "heights": [31, 0, 32, 33, 1, 15, 16, 17, 2],
+    "one_of_many": [0] * 20 + [600] + [0] * 11,
+    "each_one": [1] * 40,
+}
+
+
+@pytest.mark.parametrize("name", FEW)
+@pytest.mark.parametrize("K,N", [(8, 48), (24, 16), (256, 80), (1016, 48), (1032, 112), (2312, 48),
+                                 (264, 1008)])
+def test_few_rows_exact(name, K, N):
+    counts = FEW[name]
+    g = gen(16)
+    P, E, sp, I = rows_of(counts), len(counts), spans(counts, PAD), N // 2
+    off = offsets_of(counts, PAD)
+    # |gate|, |up| <= K: their product stays below 2^24
+    x, w = ints(g, -1, 1, P, K), ints(g, -1, 1, E, N, K)
+    inside = fill(x, sp, float("nan"))
+    y = torch.full((P, N), 77.0, dtype=BF, device=DEV)
+    moe.moe_expert_matmul(x, off, w, y=y)
+    z, _ = product64(torch.where(inside[:, None], x, 0), w, sp)
+    assert_bits(y[inside], z[inside], "y")
+    assert_rows_written(y, sp, 77.0)
+    h = torch.full((P, I), 77.0, dtype=BF, device=DEV)
+    gu = torch.full((P, N), 77.0, dtype=BF, device=DEV)
+    moe.moe_expert_gated(x, off, w, act="relu", h=h, gate_up=gu)
+    assert_bits(gu[inside], z[inside], "gate_up")
+    assert_bits(h[inside], (z[:, :I].clamp(min=0) * z[:, I:])[inside], "h")
+    assert_rows_written(h, sp, 77.0)
+    assert_rows_written(gu, sp, 77.0)
+    alone, none = moe.moe_expert_gated(x, off, w, act="relu")
+    assert none is None and torch.equal(alone[inside], h[inside])
+
+
+@pytest.mark.parametrize("name", FEW)
+@pytest.mark.parametrize("act", ["none", "silu", "gelu", "relu"])
+def test_few_rows_epilogue(name, act):
+    counts = FEW[name]
+    g = gen(17)
+    K, N = 1288, 104
+    P, E, sp = rows_of(counts), len(counts), spans(counts, PAD)
+    off = offsets_of(counts, PAD)
+    x, w = normal(g, P, K), normal(g, E, N, K, scale=K**-0.5)
+    bias, res = normal(g, E, N), normal(g, P, N)
+    y, pre = moe.moe_expert_matmul(x, off, w, bias=bias, act=act, residual=res, save_pre=True)
+    z, mag = product64(x, w, sp)
+    inside = fill(x.clone(), sp, 0)
+    for e, a, b in sp:
+        z[a:b] += bias[e].double()
+    zerr = (K + 1) * 2.0**-23 * (mag + bias.double().abs().max())
+    assert_within(pre[inside], z[inside], (HALF * z.abs() + zerr)[inside], "pre")
+    want = act64(z, act) + res.double()
+    tol = HALF * want.abs() + 1.22 * zerr + 2.0**-18 * (z.abs() + 1)
+    assert_within(y[inside], want[inside], tol[inside], "y")
+    over = res.clone()
+    moe.moe_expert_matmul(x, off, w, bias=bias, act=act, residual=over, y=over)
+    assert torch.equal(over[inside], y[inside]) and torch.equal(over[~inside], res[~inside])
