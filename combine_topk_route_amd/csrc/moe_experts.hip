@@ -880,9 +880,10 @@ __global__ __launch_bounds__(S::kThreads, 2) void matmul_kernel(
 // The forward products where few rows meet few outputs: 32 rows by 32 positions (gated: 16 gate
 // columns and the same 16 up columns) a block, the inner axis split over its 8 waves.  Each wave takes
 // every 8th piece of 32 k straight from memory into the matrix instruction's registers, kAhead pieces
-// at a time; the 8 partial sums meet in LDS and are added in the waves' order.  With a few blocks on
-// the chip the time is that of one block, and what bounds it is how often a wave waits for memory: 8
-// waves of 4 pieces wait once per 1024 k, where a wave of the 128x128 tiles does per 64.
+// at a time; the 8 partial sums meet in LDS and are added in the waves' order.  With few blocks on the
+// chip the time is that of one block, and what bounds it is how often a wave waits for memory: 8 waves
+// of 4 pieces wait once per 1024 k, where the 128x128 tiles do per 64 (16 experts of 128 x 2312, 32
+// rows: 13.1 against 7.9 us, 4 us of either the launch's).
 constexpr int kThinRows = 32, kThinCols = 32, kThinWaves = 8;
 
 template <bool GATED>
@@ -1347,16 +1348,15 @@ bool read_once(int64_t rows, int32_t E, int64_t N, int64_t K) {
   return rows <= int64_t(E) * Tall::BM && E * N * K * 2 > int64_t(256) << 20 && K % 64 == 0;
 }
 
-// Whether a forward product goes to thin_kernel: no more than 32 rows an expert, and too few half tiles
-// for one on each CU (`per_half`: the outputs' columns that one covers).  Measured, half tiles against
-// thin ones, rows spread at random: 16 experts of 128 x 2312 (20 half tiles) 512 rows 15.3 against 9.4
-// us; 2 of 3504 x 3256 (28) one row 16.0 against 9.5, (56) 64 rows 23.8 against 21.2; 8 of 1024 x 512
-// (64) 32 rows 7.0 against 7.3; 16 of 4096 x 4096 (64) 2 rows 29.3 against 13.9; 64 of 2048 x 1024 (128)
-// 8 rows 8.9 against 8.6, (256) 16 rows 12.2 against 15.8; 8 of 7168 x 1000 (448) 8 rows 18.9 against
-// 21.1; 16 of 4096 x 4096 (512) 32 rows 78 against 87.
-bool thin_tiles(int64_t rows, int32_t E, int64_t cols, int per_half) {
-  return rows <= int64_t(E) * kThinRows &&
-         row_tile_blocks(rows, E, Half::FULL, (cols + per_half - 1) / per_half) < kCus;
+// Whether a forward product goes to thin_kernel: its tiles, 32 rows by `per_tile` of the outputs'
+// `cols` columns, number at most 3 for two CUs.  Measured, products of the other shapes against thin
+// ones, rows spread at random: one expert of 512 x 1024 500 rows (256 thin tiles) 11.9 against 7.2 us,
+// of 1024 x 4096 480 rows (512) 42 against 32; 4 of 2048 x 4096 4 rows (256) 20 against 13, 64 rows
+// (384) 21 against 16, 128 rows (512) 23 against 32; 16 of 256 x 4096 512 rows (256) 22 against 18, all
+// at one expert of 16 of 128 x 2312 (128) 21 against 9; 64 of 2048 x 1024 16 rows (1024) 12 against 16,
+// all 512 at one of 16 of 1024 x 4096 (1024) 42 against 33.
+bool thin_tiles(int64_t rows, int32_t E, int64_t cols, int per_tile) {
+  return row_tile_blocks(rows, E, kThinRows, (cols + per_tile - 1) / per_tile) <= kCus * 3 / 2;
 }
 
 // run(shape) of the shape a product with weights [E, N, K] takes.
@@ -1381,7 +1381,7 @@ int moe_expert_gated(const void* x, const int32_t* expert_offsets, const void* w
   if (!aligned(x, 16) || !aligned(w_gate_up, 16) || !aligned(h, 16) || !aligned(gate_up, 16) ||
       !aligned(expert_offsets, 4))
     return MOE_ERR_ALIGNMENT;
-  if (thin_tiles(rows, E, I, Half::BN / 2))
+  if (thin_tiles(rows, E, I, kThinCols / 2))
     return launch(thin_kernel<true>,
                   row_tile_blocks(rows, E, kThinRows, (I + kThinCols / 2 - 1) / (kThinCols / 2)),
                   kThinWaves * kWave, static_cast<hipStream_t>(stream),
@@ -1408,7 +1408,7 @@ int moe_expert_matmul(const void* x, const int32_t* expert_offsets, const void* 
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(bias, 16) ||
       !aligned(residual, 16) || !aligned(pre, 16) || !aligned(expert_offsets, 4))
     return MOE_ERR_ALIGNMENT;
-  if (thin_tiles(rows, E, N, Half::BN))
+  if (thin_tiles(rows, E, N, kThinCols))
     return launch(thin_kernel<false>,
                   row_tile_blocks(rows, E, kThinRows, (N + kThinCols - 1) / kThinCols),
                   kThinWaves * kWave, static_cast<hipStream_t>(stream),

@@ -209,6 +209,8 @@ def moe_expert_matmul_backward(dy: torch.Tensor, x: torch.Tensor, expert_offsets
             raise ValueError("pre (the forward call's) is needed with an activation")
         pp = _given(pre, "pre", (rows, N), _BF16, d)
         dpre, dpp = _out(dpre, "dpre", (rows, N), _BF16, x, stream)
+    elif dpre is not None:
+        raise ValueError("dpre is written with an activation only (without one it is dy)")
     dxp = dwp = dbp = None
     wt = _dw_dtype(dw, dw_dtype)
     if need_dx or dx is not None:

@@ -494,3 +494,52 @@ def test_few_rows_epilogue(name, act):
     over = res.clone()
     moe.moe_expert_matmul(x, off, w, bias=bias, act=act, residual=over, y=over)
     assert torch.equal(over[inside], y[inside]) and torch.equal(over[~inside], res[~inside])
+
+
+@pytest.mark.parametrize("name", ["empty_between", "heights", "tall", "hot", "many"])
+@pytest.mark.parametrize("K,N", [(8, 2064), (64, 4096), (72, 2064), (120, 2064), (520, 4112), (1000, 2064)])
+def test_wide_products_exact(name, K, N):
+    """Few rows against many outputs: the tiles of 128 rows at every height."""
+    counts = COUNTS[name]
+    g = gen(18)
+    P, E, sp, I = rows_of(counts), len(counts), spans(counts, PAD), N // 2
+    off = offsets_of(counts, PAD)
+    x, w = ints(g, -1, 1, P, K), ints(g, -1, 1, E, N, K)
+    inside = fill(x, sp, float("nan"))
+    y = torch.full((P, N), 77.0, dtype=BF, device=DEV)
+    moe.moe_expert_matmul(x, off, w, y=y)
+    z, _ = product64(torch.where(inside[:, None], x, 0), w, sp)
+    assert_bits(y[inside], z[inside], "y")
+    assert_rows_written(y, sp, 77.0)
+    h = torch.full((P, I), 77.0, dtype=BF, device=DEV)
+    gu = torch.full((P, N), 77.0, dtype=BF, device=DEV)
+    moe.moe_expert_gated(x, off, w, act="relu", h=h, gate_up=gu)
+    assert_bits(gu[inside], z[inside], "gate_up")
+    assert_bits(h[inside], (z[:, :I].clamp(min=0) * z[:, I:])[inside], "h")
+    assert_rows_written(h, sp, 77.0)
+    assert_rows_written(gu, sp, 77.0)
+
+
+@pytest.mark.parametrize("name", ["heights", "hot"])
+@pytest.mark.parametrize("act", ["none", "silu", "gelu", "relu"])
+def test_wide_products_epilogue(name, act):
+    counts = COUNTS[name]
+    g = gen(19)
+    K, N = 136, 2056
+    P, E, sp = rows_of(counts), len(counts), spans(counts, PAD)
+    off = offsets_of(counts, PAD)
+    x, w = normal(g, P, K), normal(g, E, N, K, scale=K**-0.5)
+    bias, res = normal(g, E, N), normal(g, P, N)
+    y, pre = moe.moe_expert_matmul(x, off, w, bias=bias, act=act, residual=res, save_pre=True)
+    z, mag = product64(x, w, sp)
+    inside = fill(x.clone(), sp, 0)
+    for e, a, b in sp:
+        z[a:b] += bias[e].double()
+    zerr = (K + 1) * 2.0**-23 * (mag + bias.double().abs().max())
+    assert_within(pre[inside], z[inside], (HALF * z.abs() + zerr)[inside], "pre")
+    want = act64(z, act) + res.double()
+    tol = HALF * want.abs() + 1.22 * zerr + 2.0**-18 * (z.abs() + 1)
+    assert_within(y[inside], want[inside], tol[inside], "y")
+    over = res.clone()
+    moe.moe_expert_matmul(x, off, w, bias=bias, act=act, residual=over, y=over)
+    assert torch.equal(over[inside], y[inside]) and torch.equal(over[~inside], res[~inside])

@@ -292,6 +292,7 @@ def test_refusals():
         (ValueError, "bias must have", lambda: moe.moe_expert_matmul(h, off, w2, bias=normal(g, H))),
         (ValueError, "residual must be", lambda: moe.moe_expert_matmul(h, off, w2, residual=h)),
         (ValueError, "pre", lambda: moe.moe_expert_matmul_backward(y, h, off, w2, act="silu")),
+        (ValueError, "dpre is written", lambda: moe.moe_expert_matmul_backward(y, h, off, w2, dpre=y)),
         (ValueError, "dy must be", lambda: moe.moe_expert_matmul_backward(h, h, off, w2)),
         (TypeError, "dw must be", lambda: moe.moe_expert_matmul_backward(y, h, off, w2,
                                                                          dw_dtype=torch.float16)),
