@@ -122,7 +122,7 @@ __device__ __forceinline__ float act_slope(float z) {
 // f(integral_constant<int, act>): one branch in front of a loop over rows, whose code is then one
 // short piece.  With the branch inside, a tile's epilogue took 7 us longer, mostly to fetch it.
 template <typename F>
-__device__ __forceinline__ void with_act(int act, F f) {
+__host__ __device__ __forceinline__ void with_act(int act, F f) {
   if (act == MOE_ACT_SILU)
     f(std::integral_constant<int, MOE_ACT_SILU>{});
   else if (act == MOE_ACT_GELU)
@@ -1186,49 +1186,91 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(const uint16_t* dh, con
   }
 }
 
-// dpre = dy * act'(pre) and dbias[e] = its sum over the expert's rows, in a
-// fixed order: a block owns 64 columns of one expert, 32 threads a column
-// chunk, each adding every 32nd row.
+// dpre = dy * act'(pre), 8 columns per thread.
 template <int ACT>
-__global__ __launch_bounds__(256) void pre_grad_kernel(const uint16_t* dy, const uint16_t* pre,
-                                                       const int32_t* off, int64_t rows, int E,
-                                                       int N, uint16_t* dpre,
-                                                       float* dbias) {
-  __shared__ float part[32][65];
-  const int64_t strips = (N + 63) / 64;
+__global__ __launch_bounds__(256) void pre_kernel(const uint16_t* dy, const uint16_t* pre,
+                                                  const int32_t* off, int64_t rows, int E, int N,
+                                                  uint16_t* dpre) {
+  const int64_t first = off[0] < 0 ? 0 : (off[0] > rows ? rows : off[0]);
+  const int64_t last = off[E] < 0 ? 0 : (off[E] > rows ? rows : off[E]);
+  const int64_t end = last * N;
+  for (int64_t at = first * N + (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) * 8; at < end;
+       at += int64_t(gridDim.x) * blockDim.x * 8) {
+    f32x4 y0, y1, p0, p1;
+    load8(dy + at, y0, y1);
+    load8(pre + at, p0, p1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y0[i] *= act_slope<ACT>(p0[i]);
+      y1[i] *= act_slope<ACT>(p1[i]);
+    }
+    store8(dpre + at, y0, y1);
+  }
+}
+
+// The same with dbias[e], dpre's sum over the expert's rows, in a fixed order: a block owns COLS columns
+// of one expert, COLS / 8 threads a row, each thread adding every (8 THREADS / COLS)th row, then the
+// lanes of a wave by a butterfly and the waves in their order.  What bounds it with few experts is the
+// one CU's work on a strip, so strips are then narrower and blocks larger (see the launch).
+template <int ACT, int THREADS, int COLS>
+__global__ __launch_bounds__(THREADS) void pre_grad_kernel(const uint16_t* dy, const uint16_t* pre,
+                                                           const int32_t* off, int64_t rows, int E,
+                                                           int N, uint16_t* dpre, float* dbias) {
+  constexpr int kLanes = COLS / 8, kStep = THREADS / kLanes, kAhead = THREADS > 256 ? 4 : 1;
+  __shared__ float part[THREADS / kWave][COLS];
+  const int64_t strips = (N + COLS - 1) / COLS;
   for (int64_t u = blockIdx.x; u < E * strips; u += gridDim.x) {
-    const int e = int(u / strips);
-    const int c = int(u % strips) * 64 + (threadIdx.x % 8) * 8;
+    const int e = int(u / strips), strip = int(u % strips) * COLS;
+    const int c = strip + int(threadIdx.x) % kLanes * 8;
     int64_t lo, cnt;
     expert_rows(off, e, rows, lo, cnt);
-    float sum[8] = {};
+    f32x4 s0 = {}, s1 = {};
     if (c < N) {
-      for (int64_t r = threadIdx.x / 8; r < cnt; r += 32) {
-        const int64_t at = (lo + r) * N + c;
-        const u32x4 vy = *reinterpret_cast<const u32x4*>(dy + at);
-        u32x4 vp = {0u, 0u, 0u, 0u}, o;
-        if (ACT != MOE_ACT_NONE) vp = *reinterpret_cast<const u32x4*>(pre + at);
+      for (int64_t r = threadIdx.x / kLanes; r < cnt; r += kStep * kAhead) {
+        f32x4 y0[kAhead], y1[kAhead], p0[kAhead] = {}, p1[kAhead] = {};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float d0 = bf16_lo(vy[q]) * act_slope<ACT>(bf16_lo(vp[q]));
-          const float d1 = bf16_hi(vy[q]) * act_slope<ACT>(bf16_hi(vp[q]));
-          sum[2 * q] += d0;
-          sum[2 * q + 1] += d1;
-          o[q] = pack_bf16x2(d0, d1);
+        for (int i = 0; i < kAhead; ++i) {
+          y0[i] = y1[i] = f32x4{};
+          if (r + i * kStep < cnt) {
+            const int64_t at = (lo + r + i * kStep) * N + c;
+            load8(dy + at, y0[i], y1[i]);
+            if (ACT != MOE_ACT_NONE) load8(pre + at, p0[i], p1[i]);
+          }
         }
-        if (dpre != nullptr) *reinterpret_cast<u32x4*>(dpre + at) = o;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (r + i * kStep >= cnt) continue;
+          if (ACT != MOE_ACT_NONE) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              y0[i][j] *= act_slope<ACT>(p0[i][j]);
+              y1[i][j] *= act_slope<ACT>(p1[i][j]);
+            }
+            store8(dpre + (lo + r + i * kStep) * N + c, y0[i], y1[i]);
+          }
+          s0 += y0[i];
+          s1 += y1[i];
+        }
       }
     }
-    if (dbias == nullptr) continue;
-    __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 8; ++q) part[threadIdx.x / 8][(threadIdx.x % 8) * 8 + q] = sum[q];
+    for (int m = kLanes; m < kWave; m <<= 1)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s0[j] += __shfl_xor(s0[j], m);
+        s1[j] += __shfl_xor(s1[j], m);
+      }
+    __syncthreads();  // part of the strip before has been read
+    if (lane_id() < kLanes) {
+      f32x4* o = reinterpret_cast<f32x4*>(&part[threadIdx.x / kWave][lane_id() * 8]);
+      o[0] = s0;
+      o[1] = s1;
+    }
     __syncthreads();
-    const int64_t col = (u % strips) * 64 + threadIdx.x;
-    if (threadIdx.x < 64 && col < N) {
+    if (threadIdx.x < COLS && strip + int(threadIdx.x) < N) {
       float s = 0.f;
-      for (int r = 0; r < 32; ++r) s += part[r][threadIdx.x];
-      dbias[int64_t(e) * N + col] = s;
+      for (int w = 0; w < THREADS / kWave; ++w) s += part[w][threadIdx.x];
+      dbias[int64_t(e) * N + strip + threadIdx.x] = s;
     }
   }
 }
@@ -1513,16 +1555,29 @@ int moe_expert_matmul_backward(const void* dy, const void* pre, const void* x,
     return MOE_ERR_ALIGNMENT;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const void* d = has_act ? dpre : dy;
-  if ((has_act && rows > 0) || dbias) {
-    auto kern = act == MOE_ACT_SILU   ? pre_grad_kernel<MOE_ACT_SILU>
-                : act == MOE_ACT_GELU ? pre_grad_kernel<MOE_ACT_GELU>
-                : act == MOE_ACT_RELU ? pre_grad_kernel<MOE_ACT_RELU>
-                                      : pre_grad_kernel<MOE_ACT_NONE>;
-    st = launch(kern, int64_t(E) * ((N + 63) / 64), 256, s,
-                static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(pre),
-                expert_offsets, rows, E, N,
-                has_act ? static_cast<uint16_t*>(dpre) : nullptr, dbias);
-  }
+  const uint16_t* dyv = static_cast<const uint16_t*>(dy);
+  const uint16_t* prev = static_cast<const uint16_t*>(pre);
+  uint16_t* dprev = static_cast<uint16_t*>(dpre);
+  with_act(act, [&](auto a) {
+    if (dbias) {
+      const auto sums = [&](auto kern, int threads, int cols) {
+        return launch(kern, int64_t(E) * ((N + cols - 1) / cols), threads, s, dyv, prev,
+                      expert_offsets, rows, E, N, dprev, dbias);
+      };
+      // Strips of 64 columns, of 256 threads where there are two a CU, of 1024 where there are fewer;
+      // where these would be under 64, strips of 16 columns.  Measured, gelu, in this order: 60
+      // experts of 1024 columns (960 strips) 16384 rows 23 / 29 / 71 us, 256 of 2048 (8192) 1024 rows
+      // 13 / 67 / 355, 8 of 7168 (896) 16384 rows 157 / 163 / 463, 8 of 1024 (128) 51 / 33 / 57, one of
+      // 4096 (64) 8192 rows 180 / 108 / 106, one of 520 (9) 295 / 128 / 39.
+      const int64_t strips = int64_t(E) * ((N + 63) / 64);
+      st = strips >= 2 * kCus ? sums(pre_grad_kernel<a, 256, 64>, 256, 64)
+           : strips >= 64     ? sums(pre_grad_kernel<a, 1024, 64>, 1024, 64)
+                              : sums(pre_grad_kernel<a, 1024, 16>, 1024, 16);
+    } else if (has_act && rows > 0) {
+      st = launch(pre_kernel<a>, (rows * (N / 8) + 255) / 256, 256, s, dyv, prev, expert_offsets,
+                  rows, E, N, dprev);
+    }
+  });
   if (st != MOE_OK) return st;
   return product_grads(d, x, expert_offsets, w, rows, E, N, K, dx, dw, dw_f32, s);
 }

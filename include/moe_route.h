@@ -368,7 +368,8 @@ int moe_combine(const void* y, const int32_t* pair_row, const float* topk_w,
  *  - expert_offsets [E+1] int32 is read on the device.  Offsets outside
  *    [0, rows] are held to it; an expert whose end is not past its start has
  *    no rows.  Rows outside every expert (behind expert_offsets[E]) are left
- *    as they were in every output.
+ *    as they were in every output.  Offsets ascend; where they do not, rows
+ *    that two experts claim get values of either, or none.
  *  - Features (H, I, K, N) are multiples of 8 between 8 and 2^20; every bf16
  *    pointer is 16-byte aligned.  1 <= E <= 1024.  Sizes whose tiles (128 rows
  *    or features by 64) would number 2^31 or more are MOE_ERR_INVALID_ARG; no

@@ -543,3 +543,41 @@ def test_wide_products_epilogue(name, act):
     over = res.clone()
     moe.moe_expert_matmul(x, off, w, bias=bias, act=act, residual=over, y=over)
     assert torch.equal(over[inside], y[inside]) and torch.equal(over[~inside], res[~inside])
+
+
+# dbias's strips: 16 columns a block, 64 columns by 1024 threads, 64 columns by 256.
+@pytest.mark.parametrize("counts,N", [
+    ([700], 8), ([3, 0, 515], 72), ([2100, 31, 0, 1], 24), ([127, 128, 129, 5], 1032), ([600, 1], 4104),
+    ([(5 * e) % 9 for e in range(130)], 264),
+], ids=["one", "few", "long", "middle", "two", "many"])
+@pytest.mark.parametrize("act", ["none", "silu", "gelu", "relu"])
+def test_bias_gradient(counts, N, act):
+    g = gen(20)
+    P, E, sp, K = rows_of(counts), len(counts), spans(counts, PAD), 8
+    off = offsets_of(counts, PAD)
+    x, w = normal(g, P, K), normal(g, E, N, K)
+    dy, pre = normal(g, P, N), normal(g, P, N, scale=2.0)
+    inside = fill(dy, sp, float("nan"))
+    fill(pre, sp, float("inf"))
+    dpre = None if act == "none" else torch.full((P, N), 77.0, dtype=BF, device=DEV)
+    dbias = torch.full((E, N), 77.0, device=DEV)
+    kw = dict(act=act, pre=None if act == "none" else pre, need_dx=False, need_dw=False)
+    moe.moe_expert_matmul_backward(dy, x, off, w, dpre=dpre, dbias=dbias, **kw)
+    d = dy.double() * slope64(pre.double(), act)
+    # the slope's own fp32 arithmetic is within 2^-18 of 1 + |pre|; a sum of n terms within n 2^-23
+    derr = 2.0**-18 * (1 + pre.double().abs()) * dy.double().abs() + 2.0**-23 * d.abs()
+    if act == "none":
+        derr = torch.zeros_like(d)
+    for e, a, b in sp:
+        want = d[a:b].sum(0)
+        tol = derr[a:b].sum(0) + (b - a) * 2.0**-23 * d[a:b].abs().sum(0)
+        assert_within(dbias[e], want, tol, f"dbias of expert {e}")
+    if act != "none":
+        assert_within(dpre[inside], d[inside], (HALF * d.abs() + derr * 1.01)[inside], "dpre")
+        assert_rows_written(dpre, sp, 77.0)
+        alone = torch.full((P, N), 77.0, dtype=BF, device=DEV)
+        moe.moe_expert_matmul_backward(dy, x, off, w, dpre=alone, **kw)
+        assert torch.equal(alone, dpre)
+    again = torch.empty_like(dbias)
+    moe.moe_expert_matmul_backward(dy, x, off, w, dbias=again, **kw)
+    assert torch.equal(again, dbias)
