@@ -1564,13 +1564,14 @@ int moe_expert_matmul_backward(const void* dy, const void* pre, const void* x,
         return launch(kern, int64_t(E) * ((N + cols - 1) / cols), threads, s, dyv, prev,
                       expert_offsets, rows, E, N, dprev, dbias);
       };
-      // Strips of 64 columns, of 256 threads where there are two a CU, of 1024 where there are fewer;
-      // where these would be under 64, strips of 16 columns.  Measured, gelu, in this order: 60
+      // Strips of 64 columns, of 256 threads where there are two a CU or few rows an expert (16 experts
+      // of 1288 columns, 300 rows: 6.2 against 7.2 us with 1024), of 1024 where there are fewer; where
+      // these would be under 64, strips of 16 columns.  Measured, gelu, in this order: 60
       // experts of 1024 columns (960 strips) 16384 rows 23 / 29 / 71 us, 256 of 2048 (8192) 1024 rows
       // 13 / 67 / 355, 8 of 7168 (896) 16384 rows 157 / 163 / 463, 8 of 1024 (128) 51 / 33 / 57, one of
       // 4096 (64) 8192 rows 180 / 108 / 106, one of 520 (9) 295 / 128 / 39.
       const int64_t strips = int64_t(E) * ((N + 63) / 64);
-      st = strips >= 2 * kCus ? sums(pre_grad_kernel<a, 256, 64>, 256, 64)
+      st = strips >= 2 * kCus || rows <= int64_t(E) * 64 ? sums(pre_grad_kernel<a, 256, 64>, 256, 64)
            : strips >= 64     ? sums(pre_grad_kernel<a, 1024, 64>, 1024, 64)
                               : sums(pre_grad_kernel<a, 1024, 16>, 1024, 16);
     } else if (has_act && rows > 0) {
